@@ -14,6 +14,9 @@ from ._lib import (  # noqa: F401
     KvCalibOps,
     KvCalibrator,
     KvTarget,
+    attn_prefill,
+    fp8_attn_decode,
+    fp8_attn_decode_workspace_size,
     fp8_block_quant,
     fp8_e4m3_encode,
     fp8_group_quant,
@@ -21,10 +24,13 @@ from ._lib import (  # noqa: F401
     fp8_kv_read,
     fp8_kv_write,
     fp8_kv_write_amax,
+    fp8_qk_norm_rope_kv_write,
     fp8_quant_w8a8_gemm_grouped,
     load,
     strerror,
+    attn_workspace,
     gemm_workspace,
+    qk_norm_rope,
     w8a8_block_gemm,
     w8a8_block_gemm_noalloc,
     w8a8_block_gemm_workspace_size,

@@ -7,6 +7,7 @@ a missing or unloadable library raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -27,6 +28,8 @@ EXPORTS = (
     "w8a8_block_gemm_prefill", "w8a8_block_gemm_grouped",
     "fp8_quant_w8a8_gemm_grouped", "w8a16_block_gemv", "w8a16_block_gemv_grouped",
     "fp8_kv_write", "fp8_kv_write_amax", "fp8_kv_read", "fp8_kv_amax",
+    "qk_norm_rope", "fp8_qk_norm_rope_kv_write", "attn_prefill",
+    "fp8_attn_decode_workspace_size", "fp8_attn_decode",
     "fp8q_kv_calib_create", "fp8q_kv_calib_create_with_ops", "fp8q_kv_calib_observe",
     "fp8q_kv_calib_decide", "fp8q_kv_calib_scales", "fp8q_kv_calib_state",
     "fp8q_kv_calib_destroy",
@@ -132,6 +135,18 @@ def load() -> ctypes.CDLL:
         "fp8_kv_read": (ctypes.c_int, [P, P, P, I32, I32, I32, I32, I64, F32, F32, P, P,
                                        I32, I32, I64, P]),
         "fp8_kv_amax": (ctypes.c_int, [P, P, I64, P, P]),
+        "qk_norm_rope": (ctypes.c_int, [P, P, P, P, F32, P, P, I64, I32, I32, I32, I32, I32, I32,
+                                        I64, I64, P, P, I64, I64, P]),
+        "fp8_qk_norm_rope_kv_write": (ctypes.c_int, [P, P, P, P, P, F32, P, P, I64, I32, I32, P, P,
+                                                     P, I32, I32, I32, I32, I32, I64, F32, F32,
+                                                     I64, I64, I64, I64, P, P, I64, I64, P]),
+        "attn_prefill": (ctypes.c_int, [P, P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, F32,
+                                        I32, I64, I64, I64, I64, P]),
+        "fp8_attn_decode_workspace_size": (ctypes.c_int, [I32, I32, I32, I32,
+                                                          ctypes.POINTER(ctypes.c_uint64)]),
+        "fp8_attn_decode": (ctypes.c_int, [P, P, P, P, P, P, P, I32, I32, I64, I32, I32, I32, I32,
+                                           I64, F32, F32, F32, I64, I64, I64, P, ctypes.c_uint64,
+                                           P]),
         "fp8q_kv_calib_create": (ctypes.c_int, [I32, F32, F32, ctypes.POINTER(P)]),
         "fp8q_kv_calib_create_with_ops": (ctypes.c_int, [I32, F32, F32,
                                                          ctypes.POINTER(KvCalibOps),
@@ -548,6 +563,257 @@ def fp8_kv_amax(k: torch.Tensor, v: torch.Tensor, amax2: torch.Tensor,
                             current_stream(k.device) if stream is None else stream)
     check("fp8_kv_amax", st)
     return amax2
+
+
+def _head_rows(t: torch.Tensor, name: str, heads: int, head_dim: int):
+    """(rows, row stride) of a [tokens, heads * head_dim] or [tokens, heads, head_dim] tensor
+    whose rows are packed (a column view of a wider buffer is fine)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    e = heads * head_dim
+    if not (t.dim() == 2 and t.shape[1] == e or
+            t.dim() == 3 and tuple(t.shape[1:]) == (heads, head_dim)):
+        raise ValueError(f"{name} must be [tokens, {heads} * {head_dim}] or [tokens, {heads}, "
+                         f"{head_dim}] (got {tuple(t.shape)})")
+    n = t.shape[0]
+    if n and not t[0].is_contiguous():
+        raise ValueError(f"{name}'s rows must be packed")
+    return n, t.stride(0) if n > 1 else e
+
+
+def _on_stream(stream, device):
+    """Allocations and fills inside go to `stream` (the current one when None)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device))
+
+
+def _same_device(where, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != where:
+            raise ValueError(f"{name} is on {t.device}, not on {where}")
+
+
+def _norm_rope(fn, q, k, v, positions, cos_sin, num_q_heads, num_kv_heads, head_dim, q_weight,
+               k_weight, eps, interleaved, q_out, k_out, cache, stream):
+    t, qs = _head_rows(q, "q", num_q_heads, head_dim)
+    tk, ks = _head_rows(k, "k", num_kv_heads, head_dim)
+    rows = {"k": tk}
+    with _on_stream(stream, q.device):
+        if q_out is None:
+            q_out = torch.zeros((t, num_q_heads * head_dim), dtype=torch.bfloat16, device=q.device)
+        if k_out is None and cache is None:
+            k_out = torch.zeros((t, num_kv_heads * head_dim), dtype=torch.bfloat16, device=q.device)
+    rows["q_out"], qos = _head_rows(q_out, "q_out", num_q_heads, head_dim)
+    kos = num_kv_heads * head_dim
+    if k_out is not None:
+        rows["k_out"], kos = _head_rows(k_out, "k_out", num_kv_heads, head_dim)
+    if v is not None:
+        rows["v"], vs = _head_rows(v, "v", num_kv_heads, head_dim)
+    if (positions is None) != (cos_sin is None):
+        raise ValueError("pass both positions and cos_sin, or neither")
+    npos, rot = 0, 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [num_positions, rot_dim]")
+        npos, rot = cos_sin.shape
+        rows["positions"] = positions.numel()
+    if cache is not None:
+        rows["slot_mapping"] = cache["slots"].numel()
+    for name, n in rows.items():
+        if n != t:
+            raise ValueError(f"{name} has {n} rows, q has {t}")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and w.numel() != head_dim:
+            raise ValueError(f"{name} must hold head_dim values")
+    _same_device(q.device, k=k, v=v, positions=positions, cos_sin=cos_sin, q_weight=q_weight,
+                 k_weight=k_weight, q_out=q_out, k_out=k_out,
+                 **({} if cache is None else {"k_cache": cache["k"], "v_cache": cache["v"],
+                                              "slot_mapping": cache["slots"]}))
+
+    def opt(x, name, dtype):
+        return None if x is None else _dev(x, name, dtype)
+
+    head = [opt(q_weight, "q_weight", _BF16), opt(k_weight, "k_weight", _BF16), eps,
+            opt(positions, "positions", torch.int64), opt(cos_sin, "cos_sin", torch.float32),
+            npos, rot, int(bool(interleaved))]
+    qp, kp = _dev(q, "q", _BF16, False), _dev(k, "k", _BF16, False)
+    qop = _dev(q_out, "q_out", _BF16, False)
+    kop = None if k_out is None else _dev(k_out, "k_out", _BF16, False)
+    with torch.cuda.device(q.device):
+        st = current_stream(q.device) if stream is None else stream
+        if cache is None:
+            rc = load().qk_norm_rope(qp, kp, *head, t, num_q_heads, num_kv_heads, head_dim, qs, ks,
+                                     qop, kop, qos, kos, st)
+        else:
+            rc = load().fp8_qk_norm_rope_kv_write(
+                qp, kp, _dev(v, "v", _BF16, False), *head, _dev(cache["k"], "k_cache", _U8),
+                _dev(cache["v"], "v_cache", _U8), _dev(cache["slots"], "slot_mapping", torch.int64),
+                t, num_q_heads, num_kv_heads, head_dim, cache["bs"], cache["blocks"],
+                cache["k_scale"], cache["v_scale"], qs, ks, vs, cache["stride"], qop, kop, qos, kos,
+                st)
+    check(fn, rc)
+    return q_out, k_out
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor | None,
+                 cos_sin: torch.Tensor | None, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                 q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                 eps: float = 1e-6, interleaved: bool = False, q_out: torch.Tensor | None = None,
+                 k_out: torch.Tensor | None = None, stream: int | None = None):
+    """RMS norm of each query and key head, then rotary positions: (q_out, k_out), bf16.
+    cos_sin: fp32 [num_positions, rot_dim], cosines then sines; rot_dim <= head_dim rotates the
+    head's first part; None for both positions and cos_sin: norms alone.  Rows of tokens whose
+    position is outside the table are left as they were (zeros when allocated here).  q_out may
+    be q and k_out may be k."""
+    return _norm_rope("qk_norm_rope", q, k, None, positions, cos_sin, num_q_heads, num_kv_heads,
+                      head_dim, q_weight, k_weight, eps, interleaved, q_out, k_out, None, stream)
+
+
+def fp8_qk_norm_rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                              positions: torch.Tensor | None, cos_sin: torch.Tensor | None,
+                              k_cache: torch.Tensor, v_cache: torch.Tensor,
+                              slot_mapping: torch.Tensor, num_q_heads: int, num_kv_heads: int,
+                              head_dim: int, block_size: int, k_scale: float, v_scale: float,
+                              q_weight: torch.Tensor | None = None,
+                              k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                              interleaved: bool = False, q_out: torch.Tensor | None = None,
+                              k_out: torch.Tensor | None = None, cache_stride: int | None = None,
+                              stream: int | None = None) -> torch.Tensor:
+    """qk_norm_rope, and fp8_kv_write of the rotated keys and of v, in one pass; returns q_out.
+    k_out, if given, receives the bf16 keys (for attn_prefill, or a calibration window)."""
+    if cache_stride is None:
+        cache_stride = block_size * num_kv_heads * head_dim
+    blocks = _kv_num_blocks(k_cache, v_cache, cache_stride)
+    cache = dict(k=k_cache, v=v_cache, slots=slot_mapping, bs=block_size, blocks=blocks,
+                 stride=cache_stride, k_scale=k_scale, v_scale=v_scale)
+    return _norm_rope("fp8_qk_norm_rope_kv_write", q, k, v, positions, cos_sin, num_q_heads,
+                      num_kv_heads, head_dim, q_weight, k_weight, eps, interleaved, q_out, k_out,
+                      cache, stream)[0]
+
+
+def _check_lse(lse, rows, heads):
+    if lse is not None and tuple(lse.shape) != (rows, heads):
+        raise ValueError(f"lse must be [{rows}, {heads}]")
+
+
+def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                 num_q_heads: int, num_kv_heads: int, head_dim: int,
+                 cu_seqlens_k: torch.Tensor | None = None, softmax_scale: float | None = None,
+                 causal: bool = True, out: torch.Tensor | None = None,
+                 lse: torch.Tensor | None = None, stream: int | None = None) -> torch.Tensor:
+    """Attention over packed prompts: q [tokens, Hq * D], k / v [tokens, Hkv * D] bf16, int32
+    cu_seqlens [num_seqs + 1] on the device (cu_seqlens_k: the queries' own when None; longer
+    sequences of keys put the queries at their end).  softmax_scale: head_dim ** -0.5 when None.
+    Rows outside every sequence are left as they were (zeros when allocated here); lse, if given,
+    is fp32 [tokens, Hq]."""
+    tq, qs = _head_rows(q, "q", num_q_heads, head_dim)
+    tk, ks = _head_rows(k, "k", num_kv_heads, head_dim)
+    tv, vs = _head_rows(v, "v", num_kv_heads, head_dim)
+    if cu_seqlens_k is None:
+        cu_seqlens_k = cu_seqlens_q
+    if tv != tk:
+        raise ValueError(f"k has {tk} rows, v has {tv}")
+    if cu_seqlens_q.numel() < 1 or cu_seqlens_k.numel() != cu_seqlens_q.numel():
+        raise ValueError("cu_seqlens_q and cu_seqlens_k must hold num_seqs + 1 entries each")
+    if out is None:
+        with _on_stream(stream, q.device):
+            out = torch.zeros((tq, num_q_heads * head_dim), dtype=torch.bfloat16, device=q.device)
+    to, os_ = _head_rows(out, "out", num_q_heads, head_dim)
+    if to != tq:
+        raise ValueError(f"out has {to} rows, q has {tq}")
+    _check_lse(lse, tq, num_q_heads)
+    _same_device(q.device, k=k, v=v, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, out=out,
+                 lse=lse)
+    scale = head_dim ** -0.5 if softmax_scale is None else softmax_scale
+    ptrs = [_dev(q, "q", _BF16, False), _dev(k, "k", _BF16, False), _dev(v, "v", _BF16, False),
+            _dev(cu_seqlens_q, "cu_seqlens_q", torch.int32),
+            _dev(cu_seqlens_k, "cu_seqlens_k", torch.int32), _dev(out, "out", _BF16, False),
+            None if lse is None else _dev(lse, "lse", torch.float32)]
+    with torch.cuda.device(q.device):
+        rc = load().attn_prefill(*ptrs, cu_seqlens_q.numel() - 1, tq, tk, num_q_heads, num_kv_heads,
+                                 head_dim, scale, int(bool(causal)), qs, ks, vs, os_,
+                                 current_stream(q.device) if stream is None else stream)
+    check("attn_prefill", rc)
+    return out
+
+
+def fp8_attn_decode_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int,
+                                   head_dim: int) -> int:
+    """Bytes of workspace fp8_attn_decode needs for this shape on the current device."""
+    b = ctypes.c_uint64()
+    check("fp8_attn_decode_workspace_size",
+          load().fp8_attn_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                                ctypes.byref(b)))
+    return b.value
+
+
+_ATTN_WORKSPACES = {}  # (device index, stream, shape) -> uint8 tensor whose counts are zero
+
+
+def attn_workspace(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int, device=None,
+                   stream: int | None = None) -> torch.Tensor:
+    """A zero-filled workspace for fp8_attn_decode calls of this shape on `stream`, kept and
+    reused.  While a graph is being captured a new one is made instead, filled within the capture
+    and held by the graph's own memory, so that no two graphs share one."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with torch.cuda.device(dev), _on_stream(stream, dev):
+        need = max(fp8_attn_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim), 256)
+        if torch.cuda.is_current_stream_capturing():
+            return torch.zeros(need, dtype=torch.uint8, device=dev)
+        key = (dev.index, current_stream(dev), num_seqs, num_q_heads, num_kv_heads, head_dim)
+        ws = _ATTN_WORKSPACES.get(key)
+        if ws is None:
+            ws = _ATTN_WORKSPACES[key] = torch.zeros(need, dtype=torch.uint8, device=dev)
+        return ws
+
+
+def fp8_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    block_tables: torch.Tensor, context_lens: torch.Tensor, num_q_heads: int,
+                    num_kv_heads: int, head_dim: int, block_size: int, k_scale: float,
+                    v_scale: float, softmax_scale: float | None = None,
+                    out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                    cache_stride: int | None = None, workspace: torch.Tensor | None = None,
+                    stream: int | None = None) -> torch.Tensor:
+    """Single-token attention over the paged E4M3 cache: q [num_seqs, Hq * D] bf16, int32
+    block_tables [num_seqs, max_blocks] and context_lens [num_seqs] (the token's own position
+    included, written before).  softmax_scale: head_dim ** -0.5 when None; lse, if given, is fp32
+    [num_seqs, Hq].  workspace: zero-filled, of fp8_attn_decode_workspace_size bytes, used for
+    calls of this shape; by default attn_workspace's."""
+    n, qs = _head_rows(q, "q", num_q_heads, head_dim)
+    cs = block_size * num_kv_heads * head_dim if cache_stride is None else cache_stride
+    blocks = _kv_num_blocks(k_cache, v_cache, cs)
+    if block_tables.dim() != 2 or block_tables.shape[0] != n or context_lens.numel() != n:
+        raise ValueError("block_tables must be [num_seqs, max_blocks], context_lens [num_seqs]")
+    width = block_tables.shape[1]
+    if n and width and not block_tables[0].is_contiguous():
+        raise ValueError("block_tables' rows must be packed")
+    if out is None:
+        with _on_stream(stream, q.device):
+            out = torch.empty((n, num_q_heads * head_dim), dtype=torch.bfloat16, device=q.device)
+    to, os_ = _head_rows(out, "out", num_q_heads, head_dim)
+    if to != n:
+        raise ValueError(f"out has {to} rows, q has {n}")
+    _check_lse(lse, n, num_q_heads)
+    _same_device(q.device, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                 context_lens=context_lens, out=out, lse=lse, workspace=workspace)
+    scale = head_dim ** -0.5 if softmax_scale is None else softmax_scale
+    ptrs = [_dev(q, "q", _BF16, False), _dev(k_cache, "k_cache", _U8), _dev(v_cache, "v_cache", _U8),
+            _dev(block_tables, "block_tables", torch.int32, False),
+            _dev(context_lens, "context_lens", torch.int32), _dev(out, "out", _BF16, False),
+            None if lse is None else _dev(lse, "lse", torch.float32)]
+    if n == 0:
+        return out
+    with torch.cuda.device(q.device):
+        st = current_stream(q.device) if stream is None else stream
+        if workspace is None:
+            workspace = attn_workspace(n, num_q_heads, num_kv_heads, head_dim, q.device, st)
+        rc = load().fp8_attn_decode(*ptrs, n, width, block_tables.stride(0) if n > 1 else width,
+                                    num_q_heads, num_kv_heads, head_dim, block_size, blocks, k_scale,
+                                    v_scale, scale, qs, os_, cs, _dev(workspace, "workspace", torch.uint8),
+                                    workspace.numel(), st)
+    check("fp8_attn_decode", rc)
+    return out
 
 
 class KvCalibrator:

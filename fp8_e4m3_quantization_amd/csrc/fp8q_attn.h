@@ -1,0 +1,64 @@
+// fp8q_attn.h -- what the attention kernels share: vector types, lane exchanges, and the search
+// for a workgroup's piece of work in a batch whose lengths only the device knows.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fp8q_device.h"
+
+namespace fp8q {
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef unsigned v2u __attribute__((ext_vector_type(2)));
+typedef unsigned v4u __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+__device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
+
+// A running reference of a softmax moves only when a score exceeds it by more than this many
+// powers of two: exp2 of what lies above it then reaches at most 2^8, far inside binary32, and
+// the sums need no rescaling in between (any reference gives the same quotient).
+constexpr float kSoftmaxSlack = 8.0f;
+
+// A pair of values combined over lanes l and l ^ 32 (l ^ 16): the swap leaves one half's (row's)
+// value in each of the two results, in every lane.
+__device__ __forceinline__ float max_over_halves(float v) {
+  const v2u r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_over_halves(float v) {
+  const v2u r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float max_over_rows(float v) {
+  const v2u r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return max_over_halves(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+__device__ __forceinline__ float sum_over_rows(float v) {
+  const v2u r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return sum_over_halves(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+}
+
+// Sum over the wave of one int per lane.
+__device__ __forceinline__ int wave_sum(int v) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// Inclusive prefix sum over the wave.
+__device__ __forceinline__ int wave_prefix(int v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+}  // namespace fp8q

@@ -340,6 +340,119 @@ int fp8_kv_read(const uint8_t* k_cache, const uint8_t* v_cache, const int64_t* s
 int fp8_kv_amax(const uint16_t* k, const uint16_t* v, int64_t n_elems, float* amax2,
                 hipStream_t stream);
 
+/* -------------------------------- head norms, rotary positions and the paged write
+ * The step between the QKV projection and attention.  For every token t < num_tokens with
+ * 0 <= positions[t] < num_positions (other tokens are padding: nothing of theirs is written)
+ * and every query and key head row x of D = head_dim values, in binary32:
+ *   n[i] = x[i] * w[i] / sqrt(mean(x^2) + eps)   (w: q_weight / k_weight; NULL: n = x)
+ *   pairs (a, b) = (i, i + R/2), or (2i, 2i + 1) when interleaved, i < R/2, R = rot_dim, with
+ *   c = cos_sin[positions[t]][i], s = cos_sin[positions[t]][R/2 + i]:
+ *     y[a] = n[a] * c - n[b] * s,  y[b] = n[b] * c + n[a] * s;   y[i] = n[i] for i >= R
+ *   q_out / k_out = bf16_rne(y)
+ * fp8_qk_norm_rope_kv_write also writes the caches as fp8_kv_write(k_out, v, ...) would (the
+ * same bytes: the codes are made of the rounded bf16 keys, so that a calibration window's replay
+ * of staged rows leaves what the live write leaves); a token whose slot is outside the pool gets
+ * its q_out (and k_out) and no cache write.
+ *   q, k, v        device bf16 rows of H*D values at q_stride / key_stride / value_stride
+ *                  (views of one projection's output are fine)
+ *   q_weight, k_weight  device bf16 [D] or NULL;  0 <= eps <= 1
+ *   positions      device int64 [num_tokens];  cos_sin  device fp32 [num_positions, rot_dim]:
+ *                  the cosines, then the sines of each position (any base, any scaling for long
+ *                  contexts).  Both may be NULL when rot_dim is 0.
+ *   q_out, k_out   device bf16 rows at their strides; each may be its input (same address and
+ *                  stride), other overlaps are not allowed; k_out may be NULL in the writing form
+ *   0 <= num_tokens; heads > 0; 0 < head_dim <= 65536; 0 <= rot_dim <= head_dim, even;
+ *   strides >= H*D, at most 2^30; the cache arguments as fp8_kv_write.
+ * The vector path needs head_dim in {32, 64, 128, 256, 512}, rot_dim % 16 == 0 (% 8 interleaved),
+ * strides % 8 == 0 and 16-byte aligned rows, weights and table (pools 8-byte aligned,
+ * cache_stride % 8 == 0); anything else takes an element-wise path with the same formula.
+ * Errors: FP8Q_EINVAL, FP8Q_ENULL, FP8Q_EALIGN, FP8Q_ELAUNCH. */
+int qk_norm_rope(const uint16_t* q, const uint16_t* k, const uint16_t* q_weight,
+                 const uint16_t* k_weight, float eps, const int64_t* positions,
+                 const float* cos_sin, int64_t num_positions, int32_t rot_dim,
+                 int32_t interleaved, int32_t num_tokens, int32_t num_q_heads,
+                 int32_t num_kv_heads, int32_t head_dim, int64_t q_stride, int64_t key_stride,
+                 uint16_t* q_out, uint16_t* k_out, int64_t q_out_stride, int64_t k_out_stride,
+                 hipStream_t stream);
+int fp8_qk_norm_rope_kv_write(const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                              const uint16_t* q_weight, const uint16_t* k_weight, float eps,
+                              const int64_t* positions, const float* cos_sin,
+                              int64_t num_positions, int32_t rot_dim, int32_t interleaved,
+                              uint8_t* k_cache, uint8_t* v_cache, const int64_t* slot_mapping,
+                              int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                              int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                              float k_scale, float v_scale, int64_t q_stride,
+                              int64_t key_stride, int64_t value_stride, int64_t cache_stride,
+                              uint16_t* q_out, uint16_t* k_out, int64_t q_out_stride,
+                              int64_t k_out_stride, hipStream_t stream);
+
+/* ------------------------------------------------ attention over whole prompts
+ * Packed sequences: sequence s has the query rows cu_seqlens_q[s] .. cu_seqlens_q[s + 1] - 1
+ * and the key / value rows cu_seqlens_k[s] .. cu_seqlens_k[s + 1] - 1 (Lq and Lk of them; Lk > Lq
+ * for a chunk of a prompt behind its history).  Query head h reads KV head h / (Hq / Hkv).
+ * Query i sees the keys j < Lk, with `causal` those with j <= i + Lk - Lq (the last query sees
+ * every key):
+ *   s[i][j] = softmax_scale * q[i] . k[j]
+ *   out[i]  = bf16_rne( sum_j exp(s[i][j]) v[j] / sum_j exp(s[i][j]) )
+ *   lse[i]  = log sum_j exp(s[i][j])
+ * A query that sees no key gets zeros and lse = -infinity.  What a query does not see does not
+ * reach it, infinities and NaN included.  FP32 products, sums and statistics; the weights are
+ * rounded to bf16 for their product with v.
+ *   q, k, v   device bf16 rows at q_stride / key_stride / value_stride elements, 16-byte aligned
+ *   out       device bf16 rows at out_stride; rows outside every sequence are left untouched
+ *   lse       device fp32 [total_q, num_q_heads], or NULL
+ *   cu_seqlens_q, cu_seqlens_k  device int32 [num_seqs + 1], ascending from 0 to at most total_q /
+ *             total_k (the rows of q and of k); entries are clamped to that range
+ *   head_dim in {64, 128, 256}; num_q_heads a multiple of num_kv_heads; strides multiples of 8,
+ *   at most 2^23; total_q, total_k <= 2^30; 0 < softmax_scale <= 2^64.
+ * Errors: FP8Q_EINVAL, FP8Q_ENULL, FP8Q_EALIGN, FP8Q_ELAUNCH. */
+int attn_prefill(const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                 const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, uint16_t* out,
+                 float* lse, int32_t num_seqs, int32_t total_q, int32_t total_k,
+                 int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                 float softmax_scale, int32_t causal, int64_t q_stride, int64_t key_stride,
+                 int64_t value_stride, int64_t out_stride, hipStream_t stream);
+
+/* ------------------------------- single-token attention over the paged E4M3 cache
+ * [staging] module doc: paged attention reads a sequence's whole history at the one scale the
+ * layer holds; fp8_kv_write defines the pool layout.  Sequence s has one query token and
+ * len = context_lens[s] cached positions (its own token's among them, written before the call);
+ * position p lies in block block_tables[s * table_stride + p / block_size] at offset
+ * p % block_size.  With K, V the E4M3 values there, of KV head h / (Hq / Hkv):
+ *   s[p] = softmax_scale * k_scale * q[s][h] . K[p]
+ *   out[s][h] = bf16_rne( v_scale * sum_p exp(s[p]) V[p] / sum_p exp(s[p]) )
+ *   lse[s][h] = log sum_p exp(s[p])
+ * len is clamped to [0, max_blocks * block_size]; positions in a block outside [0, num_blocks)
+ * do not count; a sequence without positions gets zeros and lse = -infinity.  FP32 products,
+ * sums and statistics; the weights are rounded to bf16 for their product with V.  What lies in
+ * the pools behind a sequence's end does not reach it, NaN codes included.  Results do not
+ * depend on the order in which workgroups run.
+ *   q, out      device bf16 rows at q_stride / out_stride elements, 16-byte aligned
+ *   k_cache, v_cache  device uint8 pools of num_blocks * cache_stride bytes, 16-byte aligned
+ *   block_tables      device int32 [num_seqs, table_stride], the first max_blocks of each row used
+ *   context_lens      device int32 [num_seqs];  lse  device fp32 [num_seqs, num_q_heads] or NULL
+ *   workspace   device memory of workspace_bytes >= fp8_attn_decode_workspace_size's, 256-byte
+ *               aligned; its counts (the first ceil(num_seqs * Hkv * ceil(Hq / Hkv / 16) * 4 / 256)
+ *               * 256 bytes) must be zero before the first call that uses it, e.g. all of it
+ *               zero-filled at allocation, and every call leaves them zero; a call of another
+ *               shape needs them zeroed up to its own size, which a zero-filled workspace used
+ *               only for one shape always is.  Calls sharing a workspace must not overlap in time.
+ *   head_dim in {64, 128, 256}; num_q_heads a multiple of num_kv_heads; block_size > 0;
+ *   max_blocks * block_size <= 2^30; cache_stride >= block_size*H*D, a multiple of 16; q / out
+ *   strides multiples of 8; k_scale, v_scale in [2^-64, 2^64]; 0 < softmax_scale <= 2^32.
+ * fp8_attn_decode_workspace_size: for the current device.
+ * Errors: FP8Q_EINVAL, FP8Q_ENULL, FP8Q_EALIGN, FP8Q_ELAUNCH. */
+int fp8_attn_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                   int32_t head_dim, uint64_t* bytes);
+int fp8_attn_decode(const uint16_t* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                    const int32_t* block_tables, const int32_t* context_lens, uint16_t* out,
+                    float* lse, int32_t num_seqs, int32_t max_blocks, int64_t table_stride,
+                    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                    int32_t block_size, int64_t num_blocks, float k_scale, float v_scale,
+                    float softmax_scale, int64_t q_stride, int64_t out_stride,
+                    int64_t cache_stride, void* workspace, uint64_t workspace_bytes,
+                    hipStream_t stream);
+
 /* ----------------------------------------------- online KV scale calibrator
  * [calib] module doc, PROVISIONAL_SCALE, Fp8KvCalibration::{new, observe, scales};
  * [staging] module doc ("The fix, and its tradeoff"), KvStaging::{stage,

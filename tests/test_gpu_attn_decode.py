@@ -1,0 +1,209 @@
+"""GPU parity: fp8_attn_decode against the definition in 64 bits (bounds derived in attn_ref)."""
+import math
+
+import pytest
+import torch
+
+import fp8_e4m3_quantization_amd as fq
+from tests import attn_ref
+from tests.gpu_util import DEV, need_gpu
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+
+def setup_module(_):
+    need_gpu()
+
+
+def _pools(blocks, bs, hkv, d, cs, g):
+    """Finite codes in the blocks' used part, NaN codes elsewhere."""
+    pools = []
+    for _ in range(2):
+        x = torch.full((blocks, cs), 0x7F, dtype=torch.uint8, device=DEV)
+        val = (torch.randn((blocks, bs * hkv * d), generator=g, device=DEV) * 60).clamp(-448, 448)
+        x[:, :bs * hkv * d] = val.to(torch.float8_e4m3fn).view(torch.uint8)
+        pools.append(x)
+    return pools
+
+
+def _setup(lens, hq, hkv, d, bs, seed=0, pad=0, extra=0, cols=0, nan_behind=True):
+    g = torch.Generator(device=DEV).manual_seed(seed + sum(lens) + d + bs)
+    n = len(lens)
+    need = [-(-x // bs) for x in lens]
+    blocks = sum(need) + 2
+    cs = bs * hkv * d + pad
+    kc, vc = _pools(blocks, bs, hkv, d, cs, g)
+    width = max(need) + extra
+    order = torch.randperm(blocks - 1, generator=g, device=DEV).to(torch.int32)  # last block: no one's
+    tables = torch.full((n, width + cols), blocks - 1, dtype=torch.int32, device=DEV)
+    first = 0
+    for s in range(n):
+        tables[s, :need[s]] = order[first:first + need[s]]
+        first += need[s]
+        if nan_behind and lens[s] % bs:  # stale NaN codes behind the sequence's end
+            last = int(tables[s, need[s] - 1])
+            for p in (kc, vc):
+                p[last, lens[s] % bs * hkv * d:] = 0xFF
+    for p in (kc, vc):
+        p[blocks - 1] = 0x7F
+    q = (torch.randn((n, hq * d), generator=g, device=DEV)).to(BF16)
+    return dict(q=q, kc=kc.view(-1), vc=vc.view(-1), tables=tables[:, :width], bs=bs, cs=cs, hq=hq,
+                hkv=hkv, d=d, lens=torch.tensor(lens, dtype=torch.int32, device=DEV))
+
+
+def _call(s, **kw):
+    return fq.fp8_attn_decode(s["q"], s["kc"], s["vc"], s["tables"], s["lens"], s["hq"], s["hkv"],
+                              s["d"], s["bs"], 0.02, 0.05, cache_stride=s["cs"], **kw)
+
+
+def _check(s, out, lse, scale=None):
+    scale = s["d"] ** -0.5 if scale is None else scale
+    attn_ref.decode(s["q"], s["kc"], s["vc"], s["tables"], s["lens"].tolist(), s["hq"], s["hkv"],
+                    s["d"], s["bs"], s["cs"], torch.tensor(0.02).item(), torch.tensor(0.05).item(),
+                    scale, out, lse)
+
+
+def _run(lens, hq, hkv, d, bs, **kw):
+    s = _setup(lens, hq, hkv, d, bs, **kw)
+    lse = torch.full((len(lens), hq), 3.0, device=DEV)
+    out = _call(s, lse=lse)
+    _check(s, out, lse)
+    return s, out, lse
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("bs", [1, 7, 16, 48, 128])
+def test_lengths_around_every_edge(d, bs):
+    _run([0, 1, 2, 15, 16, 17, 31, 32, 33, 63, 127, 128, 129, 160, 300], 4, 2, d, bs)
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (2, 1), (8, 8), (10, 1), (16, 1), (17, 1), (40, 4),
+                                    (36, 1), (64, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_head_groups(hq, hkv, d):
+    """Groups that fill the 16 query columns, do not, and need several row tiles."""
+    _run([5, 200, 64], hq, hkv, d, 16)
+
+
+@pytest.mark.parametrize("lens", [[20000], [9000, 3, 0, 777], [4096] * 7])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_long_histories_split_over_workgroups(lens, d):
+    s, out, lse = _run(lens, 8, 2, d, 16)
+    ws = torch.zeros(fq.fp8_attn_decode_workspace_size(len(lens), 8, 2, d), dtype=torch.uint8,
+                     device=DEV)
+    for _ in range(3):  # the same bits every time; counts back at zero
+        again = _call(s, workspace=ws)
+        assert torch.equal(again, out)
+        assert not ws[:-(-len(lens) * 2 * 4 // 256) * 256].any()
+
+
+@pytest.mark.parametrize("seqs", [63, 64, 65, 130, 300])
+def test_many_sequences(seqs):
+    _run([(i * 53) % 190 for i in range(seqs)], 4, 2, 64, 16)
+
+
+def test_padded_blocks_wide_tables_and_strided_rows():
+    s, out, lse = _run([300, 17, 64], 8, 2, 128, 16, pad=256, extra=5, cols=3)
+    wide = torch.full((3, 8 * 128 + 64), 9.0, dtype=BF16, device=DEV)
+    _call(s, out=wide[:, :8 * 128])
+    assert torch.equal(wide[:, :8 * 128], out) and (wide[:, 8 * 128:] == 9).all()
+    s["q"] = torch.cat([s["q"], s["q"]], 1)[:, :8 * 128]
+    assert torch.equal(_call(s), out)
+
+
+def test_lengths_and_blocks_out_of_range():
+    """Lengths are clamped to the table; positions in blocks that do not exist do not count."""
+    s = _setup([64, 64, 64, 64], 4, 2, 128, 16, nan_behind=False)
+    s["lens"] = torch.tensor([-3, 64, 1 << 30, 64], dtype=torch.int32, device=DEV)
+    s["tables"] = s["tables"].clone()
+    s["tables"][1, 1] = -1
+    s["tables"][1, 3] = 1 << 30
+    s["tables"][3] = s["kc"].numel() // s["cs"]
+    lse = torch.zeros((4, 4), device=DEV)
+    out = _call(s, lse=lse)
+    _check(s, out, lse)
+    assert not out[0].any() and not out[3].any()
+
+
+def test_nan_codes_that_count_reach_the_output():
+    s = _setup([40], 4, 2, 128, 16)
+    row = int(s["tables"][0, 1]) * s["cs"] + 3 * 2 * 128
+    s["vc"][row + 5] = 0x7F  # position 19, KV head 0, value 5
+    out = _call(s).view(4, 128)
+    assert torch.isnan(out[:2, 5].float()).all() and not torch.isnan(out[2:].float()).any()
+    assert int(torch.isnan(out.float()).sum()) == 2
+    s["kc"][row + 9] = 0xFF
+    out = _call(s).view(4, 128)
+    assert torch.isnan(out[:2].float()).all() and not torch.isnan(out[2:].float()).any()
+
+
+def test_empty_table_and_no_sequences():
+    s = _setup([0, 0], 4, 2, 128, 16)
+    s["tables"] = torch.zeros((2, 0), dtype=torch.int32, device=DEV)
+    lse = torch.zeros((2, 4), device=DEV)
+    assert not _call(s, lse=lse).any() and (lse == -math.inf).all()
+    none = torch.zeros((0, 4 * 128), dtype=BF16, device=DEV)
+    assert fq.fp8_attn_decode(none, s["kc"], s["vc"], torch.zeros((0, 3), dtype=torch.int32, device=DEV),
+                              torch.zeros(0, dtype=torch.int32, device=DEV), 4, 2, 128, 16, 1.0,
+                              1.0).shape == (0, 512)
+
+
+@pytest.mark.parametrize("scale", [1e-4, 0.5])
+def test_scales(scale):
+    s = _setup([130, 9], 4, 1, 128, 16)
+    lse = torch.zeros((2, 4), device=DEV)
+    _check(s, _call(s, lse=lse, softmax_scale=scale), lse, scale)
+
+
+def test_cache_past_four_gib():
+    """Blocks whose byte offsets pass 2^32."""
+    bs, hkv, d = 16, 4, 128
+    cs = bs * hkv * d
+    blocks = (1 << 32) // cs + 40
+    kc = torch.empty(blocks * cs, dtype=torch.uint8, device=DEV)
+    vc = torch.empty_like(kc)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    n = 50
+    table = torch.arange(blocks - 4, blocks, device=DEV, dtype=torch.int32)[None].contiguous()
+    for p in (kc, vc):
+        x = (torch.randn(4 * cs, generator=g, device=DEV) * 50).clamp(-448, 448)
+        p[-4 * cs:] = x.to(torch.float8_e4m3fn).view(torch.uint8)
+    s = dict(q=torch.randn((1, 8 * d), generator=g, device=DEV).to(BF16), kc=kc, vc=vc, tables=table,
+             lens=torch.tensor([n], dtype=torch.int32, device=DEV), hq=8, hkv=hkv, d=d, bs=bs, cs=cs)
+    lse = torch.zeros((1, 8), device=DEV)
+    out = _call(s, lse=lse)
+    small = dict(s, kc=kc[-4 * cs:].clone(), vc=vc[-4 * cs:].clone(), tables=table - (blocks - 4))
+    _check(small, out, lse)
+
+
+def test_another_stream_and_two_replayed_graphs():
+    """Two graphs captured one after the other, replayed on two streams at once: each has its own
+    workspace; eager calls of other shapes go on between the replays."""
+    a = _setup([5000, 300], 8, 2, 128, 16)
+    b = _setup([7000, 64], 8, 2, 128, 16, seed=9)
+    want = [_call(a), _call(b)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = _call(a, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(got, want[0])
+    outs, graphs = [], []
+    for s in (a, b):
+        out = torch.zeros_like(want[0])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            _call(s, out=out)
+        outs.append(out)
+        graphs.append(graph)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for rep in range(4):
+        for o in outs:
+            o.zero_()
+        _run([(rep * 997) % 3000 + 1, 40], 4, 1, 128, 16)
+        torch.cuda.synchronize()
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
