@@ -570,15 +570,49 @@ def _head_rows(t: torch.Tensor, name: str, heads: int, head_dim: int):
     whose rows are packed (a column view of a wider buffer is fine)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    e = heads * head_dim
-    if not (t.dim() == 2 and t.shape[1] == e or
-            t.dim() == 3 and tuple(t.shape[1:]) == (heads, head_dim)):
+    e, shape = heads * head_dim, t.shape
+    if not (len(shape) == 2 and shape[1] == e or
+            len(shape) == 3 and shape[1] == heads and shape[2] == head_dim):
         raise ValueError(f"{name} must be [tokens, {heads} * {head_dim}] or [tokens, {heads}, "
-                         f"{head_dim}] (got {tuple(t.shape)})")
-    n = t.shape[0]
-    if n and not t[0].is_contiguous():
+                         f"{head_dim}] (got {tuple(shape)})")
+    n, strides = shape[0], t.stride()
+    if n and not (len(shape) == 2 and strides[1] == 1) and not t[0].is_contiguous():
         raise ValueError(f"{name}'s rows must be packed")
-    return n, t.stride(0) if n > 1 else e
+    return n, strides[0] if n > 1 else e
+
+
+def _ptr(t: torch.Tensor, name: str, dtypes, index: int, contiguous: bool = True):
+    """Address of a tensor on GPU `index`; None for None."""
+    if t is None:
+        return None
+    if t.get_device() != index or t.dtype not in dtypes or contiguous and not t.is_contiguous():
+        _dev(t, name, dtypes, contiguous)
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+    return t.data_ptr()
+
+
+def _gpu_index(t: torch.Tensor, name: str) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must live in GPU memory (got {t.device})")
+    return index
+
+
+def _call(fn: str, index: int, stream, *args) -> None:
+    """Calls the library with `index` as the current device, on `stream` (the tensors' device's
+    current one when None); raises on an error status."""
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _call(fn, index, stream, *args)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    st = getattr(load(), fn)(*args, stream)
+    if st != FP8Q_OK:
+        check(fn, st)
+
+
+_BF16S, _U8S = _BF16, _U8
+_F32S, _I32S, _I64S, _BYTES = (torch.float32,), (torch.int32,), (torch.int64,), (torch.uint8,)
 
 
 def _on_stream(stream, device):
@@ -588,22 +622,18 @@ def _on_stream(stream, device):
     return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device))
 
 
-def _same_device(where, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != where:
-            raise ValueError(f"{name} is on {t.device}, not on {where}")
-
-
 def _norm_rope(fn, q, k, v, positions, cos_sin, num_q_heads, num_kv_heads, head_dim, q_weight,
                k_weight, eps, interleaved, q_out, k_out, cache, stream):
     t, qs = _head_rows(q, "q", num_q_heads, head_dim)
     tk, ks = _head_rows(k, "k", num_kv_heads, head_dim)
     rows = {"k": tk}
-    with _on_stream(stream, q.device):
-        if q_out is None:
-            q_out = torch.zeros((t, num_q_heads * head_dim), dtype=torch.bfloat16, device=q.device)
-        if k_out is None and cache is None:
-            k_out = torch.zeros((t, num_kv_heads * head_dim), dtype=torch.bfloat16, device=q.device)
+    if q_out is None or k_out is None and cache is None:
+        with _on_stream(stream, q.device):
+            if q_out is None:
+                q_out = torch.zeros((t, num_q_heads * head_dim), dtype=torch.bfloat16, device=q.device)
+            if k_out is None and cache is None:
+                k_out = torch.zeros((t, num_kv_heads * head_dim), dtype=torch.bfloat16,
+                                    device=q.device)
     rows["q_out"], qos = _head_rows(q_out, "q_out", num_q_heads, head_dim)
     kos = num_kv_heads * head_dim
     if k_out is not None:
@@ -619,40 +649,28 @@ def _norm_rope(fn, q, k, v, positions, cos_sin, num_q_heads, num_kv_heads, head_
         npos, rot = cos_sin.shape
         rows["positions"] = positions.numel()
     if cache is not None:
-        rows["slot_mapping"] = cache["slots"].numel()
+        rows["slot_mapping"] = cache[2].numel()
     for name, n in rows.items():
         if n != t:
             raise ValueError(f"{name} has {n} rows, q has {t}")
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None and w.numel() != head_dim:
             raise ValueError(f"{name} must hold head_dim values")
-    _same_device(q.device, k=k, v=v, positions=positions, cos_sin=cos_sin, q_weight=q_weight,
-                 k_weight=k_weight, q_out=q_out, k_out=k_out,
-                 **({} if cache is None else {"k_cache": cache["k"], "v_cache": cache["v"],
-                                              "slot_mapping": cache["slots"]}))
-
-    def opt(x, name, dtype):
-        return None if x is None else _dev(x, name, dtype)
-
-    head = [opt(q_weight, "q_weight", _BF16), opt(k_weight, "k_weight", _BF16), eps,
-            opt(positions, "positions", torch.int64), opt(cos_sin, "cos_sin", torch.float32),
-            npos, rot, int(bool(interleaved))]
-    qp, kp = _dev(q, "q", _BF16, False), _dev(k, "k", _BF16, False)
-    qop = _dev(q_out, "q_out", _BF16, False)
-    kop = None if k_out is None else _dev(k_out, "k_out", _BF16, False)
-    with torch.cuda.device(q.device):
-        st = current_stream(q.device) if stream is None else stream
-        if cache is None:
-            rc = load().qk_norm_rope(qp, kp, *head, t, num_q_heads, num_kv_heads, head_dim, qs, ks,
-                                     qop, kop, qos, kos, st)
-        else:
-            rc = load().fp8_qk_norm_rope_kv_write(
-                qp, kp, _dev(v, "v", _BF16, False), *head, _dev(cache["k"], "k_cache", _U8),
-                _dev(cache["v"], "v_cache", _U8), _dev(cache["slots"], "slot_mapping", torch.int64),
-                t, num_q_heads, num_kv_heads, head_dim, cache["bs"], cache["blocks"],
-                cache["k_scale"], cache["v_scale"], qs, ks, vs, cache["stride"], qop, kop, qos, kos,
-                st)
-    check(fn, rc)
+    i = _gpu_index(q, "q")
+    args = (_ptr(q_weight, "q_weight", _BF16S, i), _ptr(k_weight, "k_weight", _BF16S, i), eps,
+            _ptr(positions, "positions", _I64S, i), _ptr(cos_sin, "cos_sin", _F32S, i), npos, rot,
+            1 if interleaved else 0)
+    qp, kp = _ptr(q, "q", _BF16S, i, False), _ptr(k, "k", _BF16S, i, False)
+    qop, kop = _ptr(q_out, "q_out", _BF16S, i, False), _ptr(k_out, "k_out", _BF16S, i, False)
+    if cache is None:
+        _call(fn, i, stream, qp, kp, *args, t, num_q_heads, num_kv_heads, head_dim, qs, ks, qop, kop,
+              qos, kos)
+    else:
+        k_cache, v_cache, slots, bs, blocks, cs, k_scale, v_scale = cache
+        _call(fn, i, stream, qp, kp, _ptr(v, "v", _BF16S, i, False), *args,
+              _ptr(k_cache, "k_cache", _U8S, i), _ptr(v_cache, "v_cache", _U8S, i),
+              _ptr(slots, "slot_mapping", _I64S, i), t, num_q_heads, num_kv_heads, head_dim, bs,
+              blocks, k_scale, v_scale, qs, ks, vs, cs, qop, kop, qos, kos)
     return q_out, k_out
 
 
@@ -685,8 +703,7 @@ def fp8_qk_norm_rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     if cache_stride is None:
         cache_stride = block_size * num_kv_heads * head_dim
     blocks = _kv_num_blocks(k_cache, v_cache, cache_stride)
-    cache = dict(k=k_cache, v=v_cache, slots=slot_mapping, bs=block_size, blocks=blocks,
-                 stride=cache_stride, k_scale=k_scale, v_scale=v_scale)
+    cache = (k_cache, v_cache, slot_mapping, block_size, blocks, cache_stride, k_scale, v_scale)
     return _norm_rope("fp8_qk_norm_rope_kv_write", q, k, v, positions, cos_sin, num_q_heads,
                       num_kv_heads, head_dim, q_weight, k_weight, eps, interleaved, q_out, k_out,
                       cache, stream)[0]
@@ -723,24 +740,19 @@ def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q
     if to != tq:
         raise ValueError(f"out has {to} rows, q has {tq}")
     _check_lse(lse, tq, num_q_heads)
-    _same_device(q.device, k=k, v=v, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, out=out,
-                 lse=lse)
-    scale = head_dim ** -0.5 if softmax_scale is None else softmax_scale
-    ptrs = [_dev(q, "q", _BF16, False), _dev(k, "k", _BF16, False), _dev(v, "v", _BF16, False),
-            _dev(cu_seqlens_q, "cu_seqlens_q", torch.int32),
-            _dev(cu_seqlens_k, "cu_seqlens_k", torch.int32), _dev(out, "out", _BF16, False),
-            None if lse is None else _dev(lse, "lse", torch.float32)]
-    with torch.cuda.device(q.device):
-        rc = load().attn_prefill(*ptrs, cu_seqlens_q.numel() - 1, tq, tk, num_q_heads, num_kv_heads,
-                                 head_dim, scale, int(bool(causal)), qs, ks, vs, os_,
-                                 current_stream(q.device) if stream is None else stream)
-    check("attn_prefill", rc)
+    i = _gpu_index(q, "q")
+    _call("attn_prefill", i, stream, _ptr(q, "q", _BF16S, i, False), _ptr(k, "k", _BF16S, i, False),
+          _ptr(v, "v", _BF16S, i, False), _ptr(cu_seqlens_q, "cu_seqlens_q", _I32S, i),
+          _ptr(cu_seqlens_k, "cu_seqlens_k", _I32S, i), _ptr(out, "out", _BF16S, i, False),
+          _ptr(lse, "lse", _F32S, i), cu_seqlens_q.numel() - 1, tq, tk, num_q_heads, num_kv_heads,
+          head_dim, head_dim ** -0.5 if softmax_scale is None else softmax_scale,
+          1 if causal else 0, qs, ks, vs, os_)
     return out
 
 
 def fp8_attn_decode_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int,
                                    head_dim: int) -> int:
-    """Bytes of workspace fp8_attn_decode needs for this shape on the current device."""
+    """Bytes of workspace that fp8_attn_decode needs for this shape on the current device."""
     b = ctypes.c_uint64()
     check("fp8_attn_decode_workspace_size",
           load().fp8_attn_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
@@ -748,24 +760,34 @@ def fp8_attn_decode_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads
     return b.value
 
 
-_ATTN_WORKSPACES = {}  # (device index, stream, shape) -> uint8 tensor whose counts are zero
+_ATTN_SIZES = {}       # (device index, shape) -> fp8_attn_decode_workspace_size there
+_ATTN_WORKSPACES = {}  # (device index, stream) -> uint8 tensor
 
 
-def attn_workspace(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int, device=None,
-                   stream: int | None = None) -> torch.Tensor:
-    """A zero-filled workspace for fp8_attn_decode calls of this shape on `stream`, kept and
-    reused.  While a graph is being captured a new one is made instead, filled within the capture
-    and held by the graph's own memory, so that no two graphs share one."""
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    with torch.cuda.device(dev), _on_stream(stream, dev):
-        need = max(fp8_attn_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim), 256)
-        if torch.cuda.is_current_stream_capturing():
-            return torch.zeros(need, dtype=torch.uint8, device=dev)
-        key = (dev.index, current_stream(dev), num_seqs, num_q_heads, num_kv_heads, head_dim)
-        ws = _ATTN_WORKSPACES.get(key)
-        if ws is None:
-            ws = _ATTN_WORKSPACES[key] = torch.zeros(need, dtype=torch.uint8, device=dev)
-        return ws
+def attn_workspace(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                   device: int | None = None, stream: int | None = None) -> torch.Tensor:
+    """A workspace for fp8_attn_decode calls of this shape on `stream`, kept and reused by its
+    later calls.  While a graph is being captured a new one is made instead, in the graph's own
+    memory, so that no two graphs share one."""
+    index = torch.cuda.current_device() if device is None else device
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return attn_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, index, stream)
+    if stream is not None and stream != torch._C._cuda_getCurrentRawStream(index):
+        with _on_stream(stream, torch.device("cuda", index)):
+            return attn_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, index)
+    shape = (index, num_seqs, num_q_heads, num_kv_heads, head_dim)
+    need = _ATTN_SIZES.get(shape)
+    if need is None:
+        need = _ATTN_SIZES[shape] = fp8_attn_decode_workspace_size(*shape[1:])
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
+    key = (index, torch._C._cuda_getCurrentRawStream(index))
+    ws = _ATTN_WORKSPACES.get(key)
+    if ws is None or ws.numel() < need:
+        ws = _ATTN_WORKSPACES[key] = torch.empty(need, dtype=torch.uint8,
+                                                 device=torch.device("cuda", index))
+    return ws
 
 
 def fp8_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -778,8 +800,8 @@ def fp8_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     """Single-token attention over the paged E4M3 cache: q [num_seqs, Hq * D] bf16, int32
     block_tables [num_seqs, max_blocks] and context_lens [num_seqs] (the token's own position
     included, written before).  softmax_scale: head_dim ** -0.5 when None; lse, if given, is fp32
-    [num_seqs, Hq].  workspace: zero-filled, of fp8_attn_decode_workspace_size bytes, used for
-    calls of this shape; by default attn_workspace's."""
+    [num_seqs, Hq].  workspace: uint8, fp8_attn_decode_workspace_size's bytes, for one call
+    at a time; by default attn_workspace's."""
     n, qs = _head_rows(q, "q", num_q_heads, head_dim)
     cs = block_size * num_kv_heads * head_dim if cache_stride is None else cache_stride
     blocks = _kv_num_blocks(k_cache, v_cache, cs)
@@ -795,24 +817,19 @@ def fp8_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     if to != n:
         raise ValueError(f"out has {to} rows, q has {n}")
     _check_lse(lse, n, num_q_heads)
-    _same_device(q.device, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-                 context_lens=context_lens, out=out, lse=lse, workspace=workspace)
-    scale = head_dim ** -0.5 if softmax_scale is None else softmax_scale
-    ptrs = [_dev(q, "q", _BF16, False), _dev(k_cache, "k_cache", _U8), _dev(v_cache, "v_cache", _U8),
-            _dev(block_tables, "block_tables", torch.int32, False),
-            _dev(context_lens, "context_lens", torch.int32), _dev(out, "out", _BF16, False),
-            None if lse is None else _dev(lse, "lse", torch.float32)]
+    i = _gpu_index(q, "q")
     if n == 0:
         return out
-    with torch.cuda.device(q.device):
-        st = current_stream(q.device) if stream is None else stream
-        if workspace is None:
-            workspace = attn_workspace(n, num_q_heads, num_kv_heads, head_dim, q.device, st)
-        rc = load().fp8_attn_decode(*ptrs, n, width, block_tables.stride(0) if n > 1 else width,
-                                    num_q_heads, num_kv_heads, head_dim, block_size, blocks, k_scale,
-                                    v_scale, scale, qs, os_, cs, _dev(workspace, "workspace", torch.uint8),
-                                    workspace.numel(), st)
-    check("fp8_attn_decode", rc)
+    if workspace is None:
+        workspace = attn_workspace(n, num_q_heads, num_kv_heads, head_dim, i, stream)
+    _call("fp8_attn_decode", i, stream, _ptr(q, "q", _BF16S, i, False),
+          _ptr(k_cache, "k_cache", _U8S, i), _ptr(v_cache, "v_cache", _U8S, i),
+          _ptr(block_tables, "block_tables", _I32S, i, False),
+          _ptr(context_lens, "context_lens", _I32S, i), _ptr(out, "out", _BF16S, i, False),
+          _ptr(lse, "lse", _F32S, i), n, width, block_tables.stride(0) if n > 1 else width,
+          num_q_heads, num_kv_heads, head_dim, block_size, blocks, k_scale, v_scale,
+          head_dim ** -0.5 if softmax_scale is None else softmax_scale, qs, os_, cs,
+          _ptr(workspace, "workspace", _BYTES, i), workspace.numel())
     return out
 
 

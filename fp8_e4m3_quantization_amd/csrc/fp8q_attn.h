@@ -43,21 +43,18 @@ __device__ __forceinline__ float sum_over_rows(float v) {
   return sum_over_halves(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
-// Sum over the wave of one int per lane.
-__device__ __forceinline__ int wave_sum(int v) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
-  return v;
+// Inclusive prefix sum over the wave: within rows of 16 lanes, then across them.
+template <int kCtrl, int kRowMask>
+__device__ __forceinline__ int dpp_add(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, kCtrl, kRowMask, 0xF, false);
 }
-
-// Inclusive prefix sum over the wave.
 __device__ __forceinline__ int wave_prefix(int v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(v, o);
-    if (lane >= o) v += u;
-  }
+  v = dpp_add<0x111, 0xF>(v);  // row_shr:1
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);  // row_bcast:15 into rows 1 and 3
+  v = dpp_add<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
   return v;
 }
 

@@ -15,11 +15,11 @@
 // so that both operands agree without an exchange.  P is rounded to bf16 for that product (at
 // most 2^-9 of each weight, under the output's own rounding).
 //
-// The positions of all sequences are cut into chunks of one length, chosen on the device so that
-// the workgroups are about as many as the device runs at once, whatever the lengths.  The four
-// waves of a workgroup take the tiles of its chunk in turn and add up in LDS; where a sequence
-// has several chunks each leaves its sums in the workspace, and the workgroup that comes last
-// adds them in the order of the chunks, so that results do not depend on who that is.
+// The histories of all sequences, laid end to end, are cut into equal shares, one for each CU,
+// whatever the lengths.  A workgroup's waves take the KV heads of its share side by side (a
+// token's heads lie side by side in the pools) and, with fewer heads than waves, its tiles in
+// turn.  A sequence that lies in several shares leaves their sums in the workspace, and a second
+// kernel adds them in the sequence's order: results do not depend on the order of workgroups.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -33,11 +33,10 @@
 namespace fp8q {
 namespace {
 
-constexpr int kDecWaves = 4;
 constexpr int kDecTile = 32;                        // positions a wave takes at a time
-constexpr int kDecStep = kDecTile * kDecWaves;      // a chunk is a multiple of this
 constexpr int kDecRows = 16;                        // query heads of a workgroup
-constexpr int kDecPerCu = 2;                        // workgroups per CU the chunks are cut for
+constexpr int kDecPerCu = 1;                        // workgroups on a CU at once
+constexpr int kJoinAtOnce = 8;                      // parts whose sums a thread has in flight
 
 struct DecodeArgs {
   const uint16_t* q;
@@ -45,27 +44,36 @@ struct DecodeArgs {
   const int32_t *tables, *lens;
   uint16_t* out;
   float* lse;
-  uint32_t* counts;  // [seqs * heads of work], zero between calls
-  float* parts;      // [units * heads of work][rows][D + 2]
+  float* parts;      // [2 * shares][heads of work][rows_most][D]: sums of weighted values
+  float2* stats;     // [2 * shares][heads of work][rows_most]: reference, sum of weights
   int64_t ts, qs, os, cs, nblocks;
   int seqs, width, hq, hkv, group, bs;
   int row_tiles;     // ceil(group / 16)
-  int units;         // chunks the grid has room for
-  int target;        // chunks wanted per head of work
+  int heads;         // heads of work: KV heads times row tiles
+  int together;      // heads of work of a workgroup: a power of two, at most its waves
+  int shares;        // places for shares of a head
+  int rows_most;     // min(group, 16)
   float scale_log2, v_scale;
 };
 
-__device__ __forceinline__ int64_t seq_len(const DecodeArgs& a, int s) {
-  const int64_t n = s < a.seqs ? a.lens[s] : 0, most = int64_t(a.width) * a.bs;
-  return n < 0 ? 0 : n > most ? most : n;
+__device__ __forceinline__ int seq_len(const DecodeArgs& a, int s) {
+  const int n = s < a.seqs ? a.lens[s] : 0;
+  return min(max(n, 0), a.width * a.bs);
 }
 
-// Values of the workspace are written and read at device scope, where every XCD sees them.
-__device__ __forceinline__ void put(float* p, float v) {
-  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ float get(const float* p) {
-  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// Sums of weights and of weighted values against a reference, and how two of them add up.
+struct Partial {
+  float ref, total;
+  float4 v;
+};
+__device__ __forceinline__ void add_to(Partial& a, const Partial& b) {
+  const float to = fmaxf(a.ref, b.ref);
+  const float f = a.ref == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(a.ref - to);
+  const float h = b.ref == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(b.ref - to);
+  a.total = a.total * f + b.total * h;
+  a.v.x = a.v.x * f + b.v.x * h; a.v.y = a.v.y * f + b.v.y * h;
+  a.v.z = a.v.z * f + b.v.z * h; a.v.w = a.v.w * f + b.v.w * h;
+  a.ref = to;
 }
 
 // Two E4M3 codes (low or high half of w) as two bf16, exact.
@@ -89,84 +97,134 @@ __device__ __forceinline__ void load_bytes(const uint8_t* p, uint32_t* w) {
   }
 }
 
-template <int D>
+// Where one sequence lies among the shares.  Steps are whole tiles of every wave that works on a
+// head; an empty sequence has one, which writes its zeros.
+struct SeqPlace {
+  int len, start, end;       // positions; its steps among all
+  int first_share, parts;    // the share of its first step; how many shares it lies in
+  // A share's place for sums is 2 u where the sequence began in an earlier share, else 2 u + 1.
+  __device__ __forceinline__ int place(int part) const {
+    return 2 * (first_share + part) + (part == 0);
+  }
+};
+struct Cut {
+  int step;  // positions
+  int each;  // steps of a share
+  int all;   // steps of all sequences
+  __device__ __forceinline__ int steps_of(int n) const { return max((n + step - 1) / step, 1); }
+  __device__ __forceinline__ int steps_at(const DecodeArgs& a, int s) const {
+    return s < a.seqs ? steps_of(seq_len(a, s)) : 0;
+  }
+  __device__ __forceinline__ SeqPlace seq_at(const DecodeArgs& a, int s, int start) const {
+    SeqPlace p;
+    p.len = __builtin_amdgcn_readfirstlane(seq_len(a, s));
+    p.start = start;
+    p.end = start + steps_of(p.len);
+    p.first_share = start / each;
+    p.parts = (p.end - 1) / each - p.first_share + 1;
+    return p;
+  }
+};
+// `first`: lane l's steps of sequence l, and their prefix sums, for the searches that follow.
+__device__ __forceinline__ Cut cut_up(const DecodeArgs& a, int waves, int* first, int* first_upto) {
+  Cut c;
+  const int lane = threadIdx.x & 63;
+  c.step = kDecTile * (waves / a.together);
+  *first = c.steps_at(a, lane);
+  *first_upto = wave_prefix(*first);
+  c.all = __builtin_amdgcn_readlane(*first_upto, 63);
+  for (int s0 = 64; s0 < a.seqs; s0 += 64)
+    c.all += __builtin_amdgcn_readlane(wave_prefix(c.steps_at(a, s0 + lane)), 63);
+  c.each = max((c.all + a.shares - 1) / a.shares, 1);
+  return c;
+}
+
+// Stores N values (4 or more) of query head `head`, from d on; the first lane of a row its lse.
+template <int D, int N>
+__device__ __forceinline__ void finish(const DecodeArgs& a, int seq, int head, int d, float ref,
+                                       float total, const float* v) {
+  const float inv = total == 0.0f ? 0.0f : a.v_scale / total;
+  uint16_t* to = a.out + seq * a.os + int64_t(head) * D + d;
+#pragma unroll
+  for (int i = 0; i < N; i += 4)
+    *reinterpret_cast<uint2*>(to + i) = make_uint2(cvt_bf16x2(v[i] * inv, v[i + 1] * inv),
+                                                   cvt_bf16x2(v[i + 2] * inv, v[i + 3] * inv));
+  if (a.lse && d == 0)
+    a.lse[int64_t(seq) * a.hq + head] =
+        total == 0.0f ? neg_inf() : (ref + __builtin_amdgcn_logf(total)) * kLn2;
+}
+
+// Waves of a workgroup: 256-wide heads need twice the registers.
+constexpr int waves_of(int d) { return d == 256 ? 4 : 8; }
+
+template <int D, int kDecWaves = waves_of(D)>
 __global__ __launch_bounds__(64 * kDecWaves, D == 256 ? 1 : 2) void decode_kernel(const DecodeArgs a) {
   constexpr int kSteps = D / 32;      // MFMAs of a 16-position score tile
   constexpr int kPieces = D / 64;     // 16-byte K loads of a lane and position
   constexpr int kOut = D / 16;        // MFMAs of the second product; bytes of V of a lane
-  constexpr int kVw = D / 64;         // dwords of them
   const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int heads = a.hkv * a.row_tiles;
-  const int hw = blockIdx.x % heads;               // head of work: KV head and row tile
-  int unit = blockIdx.x / heads;
+  // Workgroups go to the 8 XCDs in turn: where a share has several, they stay on one.
+  const int sets = a.heads / a.together;
+  const int share = blockIdx.x / (8 * sets) * 8 + blockIdx.x % 8;
+  const int hw0 = blockIdx.x / 8 % sets * a.together;  // first head of work here
+  const int turn = wave / a.together, turns = kDecWaves / a.together;
+  const int hw = hw0 + wave % a.together;          // this wave's
   const int kvh = hw / a.row_tiles;
-  const int row0 = (hw % a.row_tiles) * kDecRows;  // first query head of the group taken here
-  const int rows = min(kDecRows, a.group - row0);
+  auto rows_of = [&](int h) { return min(kDecRows, a.group - h % a.row_tiles * kDecRows); };
+  auto head_of = [&](int h) { return h / a.row_tiles * a.group + h % a.row_tiles * kDecRows; };
+  const int rows = rows_of(hw);
 
-  // Chunk length, and this unit's sequence and chunk.
-  int64_t all = 0;
+  int first_steps, first_upto;
+  const Cut cut = cut_up(a, kDecWaves, &first_steps, &first_upto);
+  int step = share * cut.each, seq_start = 0, seq = 0;
+  if (step >= cut.all) return;
+  const int share_end = min(step + cut.each, cut.all);
   for (int s0 = 0; s0 < a.seqs; s0 += 64) {
-    int64_t n = seq_len(a, s0 + lane);
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) n += __shfl_xor(n, o);
-    all += n;
-  }
-  const int64_t want = (all + a.target - 1) / a.target;
-  const int64_t chunk = max((want + kDecStep - 1) / kDecStep, int64_t(1)) * kDecStep;
-  int seq = -1, part = 0, parts = 0;
-  int64_t len = 0;
-  for (int s0 = 0; s0 < a.seqs; s0 += 64) {
-    const int64_t n = seq_len(a, s0 + lane);
-    const int c = s0 + lane < a.seqs ? int(max((n + chunk - 1) / chunk, int64_t(1))) : 0;
-    const int upto = wave_prefix(c), here = __shfl(upto, 63);
-    if (unit < here) {
-      const int j = __builtin_ctzll(__ballot(upto > unit));
+    const int n = s0 == 0 ? first_steps : cut.steps_at(a, s0 + lane);
+    const int upto = s0 == 0 ? first_upto : wave_prefix(n), here = __builtin_amdgcn_readlane(upto, 63);
+    if (step < seq_start + here) {
+      const int j = __builtin_ctzll(__ballot(upto > step - seq_start));
       seq = s0 + j;
-      parts = __shfl(c, j);
-      part = unit - (__shfl(upto, j) - parts);
-      len = __shfl(n, j);
+      seq_start += __builtin_amdgcn_readlane(upto, j) - __builtin_amdgcn_readlane(n, j);
       break;
     }
-    unit -= here;
-  }
-  if (seq < 0) return;
-  const int64_t begin = part * chunk, end = min(begin + chunk, len);
-
-  // Queries: column l % 16 is the query head; the order of the D values follows K's loads.
-  v8bf qf[kSteps];
-  {
-    const uint16_t* src = a.q + seq * a.qs + int64_t(kvh * a.group + row0 + min(col, rows - 1)) * D;
-#pragma unroll
-    for (int c = 0; c < kSteps; ++c)
-      qf[c] = __builtin_bit_cast(
-          v8bf, *reinterpret_cast<const uint4*>(src + 64 * (c >> 1) + 16 * g + 8 * (c & 1)));
+    seq_start += here;
   }
 
   __shared__ int64_t s_row[kDecWaves][kDecTile];
-  __shared__ float s_o[kDecWaves][kDecRows][D];
-  __shared__ float s_ref[kDecWaves][kDecRows], s_sum[kDecWaves][kDecRows];
+  __shared__ __attribute__((aligned(16))) v4f s_o[kDecWaves][kOut][64];
+  __shared__ float2 s_stats[kDecWaves][64];
   const int64_t e = int64_t(a.hkv) * D;
 
-  v4f o[kOut];
-#pragma unroll
-  for (int i = 0; i < kOut; ++i) o[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  float ref = neg_inf(), sum = 0.0f;
+  while (true) {  // over the share's pieces of sequences
+  const SeqPlace sp = cut.seq_at(a, seq, seq_start);
+  const int piece_end = min(sp.end, share_end);
+  const int begin = (step - seq_start) * cut.step;
+  const int end = min((piece_end - seq_start) * cut.step, sp.len);
+  const int part = share - sp.first_share;
+  const int32_t* table = a.tables + seq * a.ts;
 
-  for (int64_t p0 = begin + wave * kDecTile; p0 < end; p0 += kDecStep) {
-    // where the tile's positions lie in the pools; -1: none (behind the end, a bad block)
+  // A tile's K and V: lane (g, col) holds K of positions col and 16 + col, and kOut bytes of V
+  // of the 8 positions whose scores it will hold.  The registers of K are free for the next tile's
+  // once the scores are made, those of V once the products with the weights are, so that each
+  // loads during the other's half of the work.
+  uint4 kx[2][kPieces];
+  uint32_t vx[8][kOut / 4];
+  bool ok[8];
+  // The block number of lane l's position p0 + l (l < 32), one tile ahead of the loads that it
+  // addresses; -1: no such position.
+  auto block_of = [&](int p0) {
+    const int pos = p0 + lane;
+    return lane < kDecTile && pos < end ? table[uint32_t(pos) / uint32_t(a.bs)] : -1;
+  };
+  auto load_k = [&](int p0, int id) {
     if (lane < kDecTile) {
-      const int64_t pos = p0 + lane;
-      int64_t at = -1;
-      if (pos < end) {
-        const int64_t b = pos / a.bs;
-        const int64_t id = a.tables[seq * a.ts + b];
-        if (id >= 0 && id < a.nblocks) at = id * a.cs + (pos - b * a.bs) * e + int64_t(kvh) * D;
-      }
-      s_row[wave][lane] = at;
+      const uint32_t pos = uint32_t(p0 + lane);
+      const bool good = id >= 0 && id < a.nblocks;
+      s_row[wave][lane] = good ? id * a.cs + int64_t(pos % uint32_t(a.bs)) * e + int64_t(kvh) * D : -1;
     }
     __builtin_amdgcn_wave_barrier();
-    uint4 kx[2][kPieces];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const int64_t at = max(s_row[wave][16 * b + col], int64_t(0));
@@ -174,8 +232,8 @@ __global__ __launch_bounds__(64 * kDecWaves, D == 256 ? 1 : 2) void decode_kerne
       for (int c = 0; c < kPieces; ++c)
         kx[b][c] = *reinterpret_cast<const uint4*>(a.kc + at + 64 * c + 16 * g);
     }
-    uint32_t vx[8][kVw];
-    bool ok[8];
+  };
+  auto load_v = [&]() {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int64_t at = s_row[wave][16 * (j >> 2) + 4 * g + (j & 3)];
@@ -183,8 +241,15 @@ __global__ __launch_bounds__(64 * kDecWaves, D == 256 ? 1 : 2) void decode_kerne
       load_bytes<kOut>(a.vc + max(at, int64_t(0)) + kOut * col, vx[j]);
     }
     __builtin_amdgcn_wave_barrier();
+  };
 
-    float sc[8];
+  v8bf qf[kSteps];
+  v4f o[kOut];
+#pragma unroll
+  for (int i = 0; i < kOut; ++i) o[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  float ref = neg_inf(), sum = 0.0f;
+  float sc[8];
+  auto scores = [&]() {
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -199,6 +264,8 @@ __global__ __launch_bounds__(64 * kDecWaves, D == 256 ? 1 : 2) void decode_kerne
 #pragma unroll
       for (int r = 0; r < 4; ++r) sc[4 * b + r] = ok[4 * b + r] ? acc[r] * a.scale_log2 : neg_inf();
     }
+  };
+  auto weigh = [&]() {
     float top = sc[0];
 #pragma unroll
     for (int j = 1; j < 8; ++j) top = fmaxf(top, sc[j]);
@@ -221,15 +288,13 @@ __global__ __launch_bounds__(64 * kDecWaves, D == 256 ? 1 : 2) void decode_kerne
     }
     const v8bf pf = __builtin_bit_cast(v8bf, v4u{pw[0], pw[1], pw[2], pw[3]});
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int w = 0; w < kVw; ++w) vx[j][w] = ok[j] ? vx[j][w] : 0u;
-#pragma unroll
     for (int i = 0; i < kOut; i += 2) {  // values i and i + 1 of each lane's D/16
       uint32_t pair[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        pair[j] = (i & 2) ? e4m3x2_to_bf16<true>(vx[j][i / 4]) : e4m3x2_to_bf16<false>(vx[j][i / 4]);
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t w = ok[j] ? vx[j][i / 4] : 0u;
+        pair[j] = (i & 2) ? e4m3x2_to_bf16<true>(w) : e4m3x2_to_bf16<false>(w);
+      }
       v4u even, odd;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -239,89 +304,129 @@ __global__ __launch_bounds__(64 * kDecWaves, D == 256 ? 1 : 2) void decode_kerne
       o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, even), pf, o[i], 0, 0, 0);
       o[i + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, odd), pf, o[i + 1], 0, 0, 0);
     }
+  };
+
+  int p0 = begin + turn * kDecTile;
+  if (p0 < end) {
+    int id = block_of(p0), id_next = block_of(p0 + cut.step);
+    // Queries: column l % 16 is the query head; the order of the D values follows K's loads.
+    const uint16_t* src = a.q + seq * a.qs + int64_t(head_of(hw) + min(col, rows - 1)) * D;
+#pragma unroll
+    for (int c = 0; c < kSteps; ++c)
+      qf[c] = __builtin_bit_cast(
+          v8bf, *reinterpret_cast<const uint4*>(src + 64 * (c >> 1) + 16 * g + 8 * (c & 1)));
+    load_k(p0, id);
+    load_v();
+    while (true) {
+      const int p1 = p0 + cut.step;
+      id = id_next;
+      id_next = block_of(p1 + cut.step);
+      scores();
+      if (p1 < end) load_k(p1, id);
+      weigh();
+      if (p1 >= end) break;
+      load_v();
+      p0 = p1;
+    }
   }
 
   // o[i][r] is value kOut (4g + r) + i of query column l % 16.
   sum = sum_over_rows(sum);
+  // The waves of a head add up in pairs, the later half leaving its registers in LDS for the
+  // earlier one, which holds the same values of the same queries.
+  for (int half = turns / 2; half >= 1; half /= 2) {
+    if (turn >= half && turn < 2 * half) {
 #pragma unroll
-  for (int i = 0; i < kOut; ++i)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) s_o[wave][col][kOut * (4 * g + r) + i] = o[i][r];
-  if (g == 0) {
-    s_ref[wave][col] = ref;
-    s_sum[wave][col] = sum;
-  }
-  __syncthreads();
-
-  // The workgroup's sums: thread -> (row, 4 values) of the chunk.
-  auto finish = [&](int r, int d, float ref_all, float total, float4 v) {
-    const float inv = total == 0.0f ? 0.0f : a.v_scale / total;
-    const int64_t h = int64_t(kvh) * a.group + row0 + r;
-    *reinterpret_cast<uint2*>(a.out + seq * a.os + h * D + d) =
-        make_uint2(cvt_bf16x2(v.x * inv, v.y * inv), cvt_bf16x2(v.z * inv, v.w * inv));
-    if (a.lse && d == 0)
-      a.lse[int64_t(seq) * a.hq + h] =
-          total == 0.0f ? neg_inf() : (ref_all + __builtin_amdgcn_logf(total)) * kLn2;
-  };
-  const int64_t stride = int64_t(kDecRows) * (D + 2);
-  const int64_t first = (int64_t(blockIdx.x / heads) - part) * heads + hw;  // part 0's place
-  float* mine = a.parts + (first + int64_t(part) * heads) * stride;
-  for (int it = threadIdx.x; it < rows * (D / 4); it += 64 * kDecWaves) {
-    const int r = it / (D / 4), d = it % (D / 4) * 4;
-    float m = s_ref[0][r];
-#pragma unroll
-    for (int w = 1; w < kDecWaves; ++w) m = fmaxf(m, s_ref[w][r]);
-    float total = 0.0f;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-    for (int w = 0; w < kDecWaves; ++w) {
-      const float f = s_ref[w][r] == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(s_ref[w][r] - m);
-      total += s_sum[w][r] * f;
-      const float4 x = *reinterpret_cast<const float4*>(&s_o[w][r][d]);
-      v.x += x.x * f; v.y += x.y * f; v.z += x.z * f; v.w += x.w * f;
+      for (int i = 0; i < kOut; ++i) s_o[wave][i][lane] = o[i];
+      s_stats[wave][lane] = make_float2(ref, sum);
     }
-    if (parts == 1) {
-      finish(r, d, m, total, v);
-    } else {
-      float* p = mine + r * (D + 2);
-      put(p + d, v.x); put(p + d + 1, v.y); put(p + d + 2, v.z); put(p + d + 3, v.w);
-      if (d == 0) { put(p + D, m); put(p + D + 1, total); }
+    __syncthreads();
+    if (turn < half) {
+      const int from = wave + half * a.together;
+      const float2 st = s_stats[from][lane];
+      const float to = fmaxf(ref, st.x);
+      const float f = ref == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(ref - to);
+      const float h = st.x == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(st.x - to);
+      ref = to;
+      sum = sum * f + st.y * h;
+#pragma unroll
+      for (int i = 0; i < kOut; ++i) o[i] = o[i] * f + s_o[from][i][lane] * h;
     }
   }
-  if (parts == 1) return;
-
-  __shared__ int s_last;
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's sums are where all see them
-  __syncthreads();
-  if (threadIdx.x == 0)
-    s_last = __hip_atomic_fetch_add(a.counts + int64_t(seq) * heads + hw, 1u, __ATOMIC_RELAXED,
-                                    __HIP_MEMORY_SCOPE_AGENT) == uint32_t(parts - 1);
-  __syncthreads();
-  if (!s_last) return;
-  if (threadIdx.x == 0)
-    __hip_atomic_store(a.counts + int64_t(seq) * heads + hw, 0u, __ATOMIC_RELAXED,
-                       __HIP_MEMORY_SCOPE_AGENT);
-  for (int it = threadIdx.x; it < rows * (D / 4); it += 64 * kDecWaves) {
-    const int r = it / (D / 4), d = it % (D / 4) * 4;
-    const float* p = a.parts + first * stride + r * (D + 2);
-    float m = neg_inf(), total = 0.0f;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int c = 0; c < parts; ++c, p += heads * stride) {
-      const float pm = get(p + D), pt = get(p + D + 1);
-      const float4 x = make_float4(get(p + d), get(p + d + 1), get(p + d + 2), get(p + d + 3));
-      const float to = fmaxf(m, pm);
-      const float f = m == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(m - to);
-      const float h = pm == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(pm - to);
-      total = total * f + pt * h;
-      v.x = v.x * f + x.x * h; v.y = v.y * f + x.y * h;
-      v.z = v.z * f + x.z * h; v.w = v.w * f + x.w * h;
-      m = to;
+  if (turn == 0 && col < rows) {
+    const int64_t at = (int64_t(sp.place(part)) * a.heads + hw) * a.rows_most + col;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int d = kOut * (4 * g + r);
+      float v[kOut];
+#pragma unroll
+      for (int i = 0; i < kOut; ++i) v[i] = o[i][r];
+      if (sp.parts == 1) {
+        finish<D, kOut>(a, seq, head_of(hw) + col, d, ref, sum, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kOut; i += 4)
+          *reinterpret_cast<float4*>(a.parts + at * D + d + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        if (d == 0) a.stats[at] = make_float2(ref, sum);
+      }
     }
-    finish(r, d, m, total, v);
+  }
+  step = piece_end;
+  if (step >= share_end) break;
+  ++seq;
+  seq_start = sp.end;
+  __syncthreads();  // every wave has read this piece's sums in LDS
   }
 }
 
-constexpr int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+// Adds up the parts of the sequences that lie in several shares: one workgroup per sequence and
+// query head.  The D/4 lanes of a slot take every kSlots-th part; the slots' sums add up in order.
+template <int D, int kJoinThreads>
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(const DecodeArgs a, int waves) {
+  constexpr int kLanes = D / 4, kSlots = kJoinThreads / kLanes;
+  const int lane = threadIdx.x & 63;
+  const int head = blockIdx.x % a.hq, seq = blockIdx.x / a.hq;
+  int first_steps, first_upto;
+  const Cut cut = cut_up(a, waves, &first_steps, &first_upto);
+  int start = 0;
+  for (int s0 = 0; s0 <= seq; s0 += 64) {
+    const int n = s0 == 0 ? first_steps : cut.steps_at(a, s0 + lane);
+    const int upto = s0 == 0 ? first_upto : wave_prefix(n);
+    const int j = min(seq - s0, 63);
+    start += __builtin_amdgcn_readlane(upto, j) - (seq - s0 < 64 ? __builtin_amdgcn_readlane(n, j) : 0);
+  }
+  const SeqPlace sp = cut.seq_at(a, seq, start);
+  if (sp.parts == 1) return;
+  const int kvh = head / a.group, of_group = head - kvh * a.group;
+  const int hw = kvh * a.row_tiles + of_group / kDecRows, r = of_group % kDecRows;
+  const int slot = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
+  Partial sum = {neg_inf(), 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+  for (int c = slot; c < sp.parts; c += kSlots * kJoinAtOnce) {
+    float4 v[kJoinAtOnce];
+    float2 st[kJoinAtOnce];
+#pragma unroll
+    for (int j = 0; j < kJoinAtOnce; ++j) {
+      const int part = min(c + j * kSlots, sp.parts - 1);
+      const int64_t at = (int64_t(sp.place(part)) * a.heads + hw) * a.rows_most + r;
+      v[j] = *reinterpret_cast<const float4*>(a.parts + at * D + d);
+      st[j] = a.stats[at];
+    }
+#pragma unroll
+    for (int j = 0; j < kJoinAtOnce; ++j)
+      if (c + j * kSlots < sp.parts) add_to(sum, Partial{st[j].x, st[j].y, v[j]});
+  }
+  __shared__ __attribute__((aligned(16))) float s_v[kSlots][D];
+  __shared__ float2 s_st[kSlots];
+  *reinterpret_cast<float4*>(&s_v[slot][d]) = sum.v;
+  if (d == 0) s_st[slot] = make_float2(sum.ref, sum.total);
+  __syncthreads();
+  if (slot > 0) return;
+#pragma unroll
+  for (int u = 1; u < kSlots; ++u)
+    add_to(sum, Partial{s_st[u].x, s_st[u].y, *reinterpret_cast<const float4*>(&s_v[u][d])});
+  const float v[4] = {sum.v.x, sum.v.y, sum.v.z, sum.v.w};
+  finish<D, 4>(a, seq, head, d, sum.ref, sum.total, v);
+}
 
 int decode_shape(int32_t seqs, int32_t hq, int32_t hkv, int32_t d) {
   if (seqs < 0 || seqs > (1 << 20) || hq <= 0 || hkv <= 0 || hq % hkv != 0 || hq > 65536)
@@ -330,17 +435,26 @@ int decode_shape(int32_t seqs, int32_t hq, int32_t hkv, int32_t d) {
   return FP8Q_OK;
 }
 
-// Workgroups wanted per head of work, and the workspace that leaves room for.
-int decode_target(int heads) {
-  const int t = kDecPerCu * num_cus() / heads;
-  return t < 1 ? 1 : t;
-}
-uint64_t counts_bytes(int64_t seqs, int64_t heads) { return uint64_t(round_up(seqs * heads * 4, 256)); }
-uint64_t decode_workspace(int32_t seqs, int32_t hq, int32_t hkv, int32_t d) {
-  if (seqs == 0) return 0;
-  const int64_t heads = int64_t(hkv) * ((hq / hkv + kDecRows - 1) / kDecRows);
-  const int64_t units = int64_t(decode_target(int(heads))) + seqs;
-  return counts_bytes(seqs, heads) + uint64_t(units) * heads * kDecRows * (d + 2) * 4;
+// How a call is cut up, and the workspace that takes.
+struct DecodePlan {
+  int row_tiles, heads, together, shares, rows;
+  uint64_t parts_bytes, bytes;
+};
+DecodePlan decode_plan(int32_t hq, int32_t hkv, int32_t d) {
+  DecodePlan p = {};
+  const int group = hq / hkv;
+  p.row_tiles = (group + kDecRows - 1) / kDecRows;
+  p.heads = hkv * p.row_tiles;
+  p.rows = group < kDecRows ? group : kDecRows;
+  p.together = 1;
+  while (p.together < waves_of(d) && p.heads % (2 * p.together) == 0) p.together *= 2;
+  const int sets = p.heads / p.together;
+  p.shares = kDecPerCu * num_cus() / sets / 8 * 8;
+  if (p.shares < 8) p.shares = 8;
+  const uint64_t rows = uint64_t(2 * p.shares) * p.heads * p.rows;
+  p.parts_bytes = rows * d * 4;
+  p.bytes = p.parts_bytes + rows * 8;
+  return p;
 }
 
 }  // namespace
@@ -355,7 +469,7 @@ extern "C" int fp8_attn_decode_workspace_size(int32_t num_seqs, int32_t num_q_he
   *bytes = 0;
   const int rc = decode_shape(num_seqs, num_q_heads, num_kv_heads, head_dim);
   if (rc != FP8Q_OK) return rc;
-  *bytes = decode_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim);
+  if (num_seqs > 0) *bytes = decode_plan(num_q_heads, num_kv_heads, head_dim).bytes;
   return FP8Q_OK;
 }
 
@@ -371,7 +485,9 @@ extern "C" int fp8_attn_decode(const uint16_t* q, const uint8_t* k_cache, const 
   if (rc != FP8Q_OK) return rc;
   if (max_blocks < 0 || block_size <= 0 || num_blocks <= 0 || table_stride < max_blocks)
     return FP8Q_EINVAL;
-  if (int64_t(max_blocks) * block_size > (int64_t(1) << 30)) return FP8Q_EINVAL;
+  const int64_t most = int64_t(max_blocks) * block_size;
+  if (most > (int64_t(1) << 30) || num_seqs * (most / kDecTile + 1) > (int64_t(1) << 30))
+    return FP8Q_EINVAL;
   const int64_t eq = int64_t(num_q_heads) * head_dim, ek = int64_t(num_kv_heads) * head_dim;
   if (q_stride < eq || out_stride < eq || q_stride > (int64_t(1) << 30) ||
       out_stride > (int64_t(1) << 30) || table_stride > (int64_t(1) << 40))
@@ -389,24 +505,36 @@ extern "C" int fp8_attn_decode(const uint16_t* q, const uint8_t* k_cache, const 
       !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(lse, 4) ||
       !aligned(workspace, 256) || q_stride % 8 || out_stride % 8 || cache_stride % 16)
     return FP8Q_EALIGN;
-  if (workspace_bytes < decode_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim))
-    return FP8Q_EINVAL;
+  const DecodePlan p = decode_plan(num_q_heads, num_kv_heads, head_dim);
+  if (workspace_bytes < p.bytes) return FP8Q_EINVAL;
   DecodeArgs a = {};
   a.q = q, a.kc = k_cache, a.vc = v_cache, a.tables = block_tables, a.lens = context_lens;
   a.out = out, a.lse = lse, a.ts = table_stride, a.qs = q_stride, a.os = out_stride;
   a.cs = cache_stride, a.nblocks = num_blocks, a.seqs = num_seqs, a.width = max_blocks;
   a.hq = num_q_heads, a.hkv = num_kv_heads, a.group = num_q_heads / num_kv_heads;
-  a.bs = block_size, a.row_tiles = (a.group + kDecRows - 1) / kDecRows;
-  const int heads = a.hkv * a.row_tiles;
-  a.target = decode_target(heads);
-  a.units = a.target + num_seqs;
-  a.counts = static_cast<uint32_t*>(workspace);
-  a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + counts_bytes(num_seqs, heads));
+  a.bs = block_size, a.row_tiles = p.row_tiles, a.heads = p.heads, a.together = p.together;
+  a.shares = p.shares, a.rows_most = p.rows;
+  a.parts = static_cast<float*>(workspace);
+  a.stats = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.parts_bytes);
   a.scale_log2 = softmax_scale * k_scale * kLog2e;
   a.v_scale = v_scale;
-  const int64_t blocks = int64_t(a.units) * heads;
-  if (blocks > 0x7FFFFFFF) return FP8Q_EINVAL;
+  const int64_t blocks = int64_t(p.shares) * (p.heads / p.together);
+  const int64_t joins = int64_t(num_seqs) * num_q_heads;
+  if (blocks > 0x7FFFFFFF || joins > 0x7FFFFFFF) return FP8Q_EINVAL;
+  const int waves = waves_of(head_dim);
   auto kern = head_dim == 64 ? decode_kernel<64> : head_dim == 128 ? decode_kernel<128> : decode_kernel<256>;
-  launch(kern, dim3(unsigned(blocks)), dim3(64 * kDecWaves), 0, stream, a);
+  launch(kern, dim3(unsigned(blocks)), dim3(64 * waves), 0, stream, a);
+  if (launch_status() != FP8Q_OK) return launch_status();
+  // no history can lie in two shares: nothing to join
+  if (most <= kDecTile) return FP8Q_OK;
+  // Long rows of parts (few sequences) take many threads, short ones few: 2 sequences of 100 000
+  // positions join in 6.8 us with 512 threads a head, 9.3 us with 128; 64 of 4 000 in 11.3 and
+  // 5.8 us.
+  const bool wide = p.shares / num_seqs > 16;
+  void (*join)(DecodeArgs, int) =
+      head_dim == 64 ? (wide ? join_kernel<64, 512> : join_kernel<64, 128>)
+      : head_dim == 128 ? (wide ? join_kernel<128, 512> : join_kernel<128, 128>)
+                        : (wide ? join_kernel<256, 512> : join_kernel<256, 128>);
+  launch(join, dim3(unsigned(joins)), dim3(wide ? 512 : 128), 0, stream, a, waves);
   return launch_status();
 }

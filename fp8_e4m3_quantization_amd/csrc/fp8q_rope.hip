@@ -37,12 +37,24 @@ struct RopeArgs {
   float eps, k_scale, k_inv, v_scale, v_inv;
 };
 
+// p[i] for an index that is the same in the whole wave, through the scalar cache: the lists of
+// positions and slots are only read.
+__device__ __forceinline__ int64_t uniform_at(const int64_t* p, int64_t i) {
+  typedef const __attribute__((address_space(4))) int64_t* constant_i64;
+  return ((constant_i64)p)[i];
+}
+
 // Where token t's row lies in the pools (elements from their start), or -1: no such slot.
 __device__ __forceinline__ int64_t pool_row(const RopeArgs& a, int64_t t) {
   if (!a.slots) return -1;
-  const int64_t slot = a.slots[t];
+  const int64_t slot = uniform_at(a.slots, t);
   if (slot < 0 || slot >= a.nslots) return -1;
-  return slot / a.bs * a.cs + slot % a.bs * (int64_t(a.hkv) * a.d);
+  const int64_t e = int64_t(a.hkv) * a.d;
+  if (a.nslots <= 0x7FFFFFFF) {  // 32-bit division
+    const uint32_t b = uint32_t(slot) / uint32_t(a.bs);
+    return int64_t(b) * a.cs + int64_t(uint32_t(slot) - b * uint32_t(a.bs)) * e;
+  }
+  return slot / a.bs * a.cs + slot % a.bs * e;
 }
 
 __device__ __forceinline__ float sq_sum8(uint4 w) {
@@ -56,79 +68,103 @@ __device__ __forceinline__ void unpack8(uint4 w, float* f) {
   f[4] = bf16_lo(w.z); f[5] = bf16_hi(w.z); f[6] = bf16_lo(w.w); f[7] = bf16_hi(w.w);
 }
 
+// Sum over each aligned group of 2^kLanesLog2 lanes, in every lane of it.
+template <int kLanesLog2>
+__device__ __forceinline__ float sum_over_lanes(float v) {
+  v += dpp<0xB1>(v);                           // lane ^ 1
+  v += dpp<0x4E>(v);                           // lane ^ 2
+  if constexpr (kLanesLog2 >= 3) v += dpp<0x141>(v);  // mirror within 8 lanes
+  if constexpr (kLanesLog2 >= 4) v += dpp<0x140>(v);  // mirror within 16
+  if constexpr (kLanesLog2 >= 5) v += __shfl_xor(v, 16);
+  if constexpr (kLanesLog2 >= 6) v += __shfl_xor(v, 32);
+  return v;
+}
+
 // One workgroup per token.  L = D/8 lanes (a power of two) take a head, 8 values each, so a
 // lane loads its head chunk in one 16-byte load, a head's mean square is a reduction over
 // L neighbouring lanes, and the pair partner of a lane's chunk in the half layout is the chunk
-// of the lane rot/16 away.  A lane keeps its cosines and sines for every head of the token.
-constexpr int kRopeAhead = 4;  // heads whose loads a lane issues before it computes
+// of the lane rot/16 away, exchanged as bf16 (four words) and normed by both lanes.  A lane keeps
+// its cosines, sines and weights for every head of the token, and issues the loads of up to four
+// heads before the table's, whose address waits for the position.
+constexpr int kRopeAhead = 4;
 
 template <int kLanesLog2, bool kInterleaved>
 __global__ __launch_bounds__(1024) void rope_vec_kernel(const RopeArgs a) {
   constexpr int kLanes = 1 << kLanesLog2;
+  constexpr int kD = 8 * kLanes;
   const int c = threadIdx.x & (kLanes - 1);
   const int g = threadIdx.x >> kLanesLog2;
   const int ng = blockDim.x >> kLanesLog2;
   const int heads = a.hq + a.hkv + (a.slots ? a.hkv : 0);
-  const int d = 8 * kLanes;
   const bool turns = 8 * c < a.rot;
   const int reach = a.rot >> 4;                       // lanes between a pair's chunks
   const bool second = !kInterleaved && c >= reach;    // this chunk holds the pairs' b
-  const int partner = second ? c - reach : c + reach;
+  const int partner = turns ? (second ? c - reach : c + reach) : c;
   const uint4 ones = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
   for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-    const int64_t pos = a.rot ? a.positions[t] : 0;
+    const int64_t pos = a.rot ? uniform_at(a.positions, t) : 0;
+    uint4 x[kRopeAhead];
+    auto load = [&](int h0) {
+#pragma unroll
+      for (int u = 0; u < kRopeAhead; ++u) {
+        const int h = h0 + u * ng;
+        if (h >= heads) continue;
+        const uint16_t* src = h < a.hq ? a.q + t * a.qs + int64_t(h) * kD
+                            : h < a.hq + a.hkv ? a.k + t * a.ks + int64_t(h - a.hq) * kD
+                                               : a.v + t * a.vs + int64_t(h - a.hq - a.hkv) * kD;
+        x[u] = load16_nt(reinterpret_cast<const uint4*>(src) + c);
+      }
+    };
+    load(g);
+    uint4 qw = ones, kw = ones, qwp = ones, kwp = ones;
+    if (a.qw) {
+      qw = reinterpret_cast<const uint4*>(a.qw)[c];
+      if constexpr (!kInterleaved) qwp = reinterpret_cast<const uint4*>(a.qw)[partner];
+    }
+    if (a.kw) {
+      kw = reinterpret_cast<const uint4*>(a.kw)[c];
+      if constexpr (!kInterleaved) kwp = reinterpret_cast<const uint4*>(a.kw)[partner];
+    }
     if (a.rot && (pos < 0 || pos >= a.npos)) continue;
     const int64_t row = pool_row(a, t);
-    float cs[8], sn[8];
+    float cs[8] = {}, sn[8] = {};
     if (turns) {
       const int f0 = kInterleaved ? 4 * c : 8 * (second ? c - reach : c);
       const float* p = a.cos_sin + pos * a.rot + f0;
       const float* ps = p + (a.rot >> 1);
 #pragma unroll
       for (int i = 0; i < (kInterleaved ? 4 : 8); i += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(p + i);
-        const float4 y = *reinterpret_cast<const float4*>(ps + i);
-        cs[i] = x.x; cs[i + 1] = x.y; cs[i + 2] = x.z; cs[i + 3] = x.w;
-        sn[i] = y.x; sn[i + 1] = y.y; sn[i + 2] = y.z; sn[i + 3] = y.w;
+        const float4 u = *reinterpret_cast<const float4*>(p + i);
+        const float4 w = *reinterpret_cast<const float4*>(ps + i);
+        cs[i] = u.x; cs[i + 1] = u.y; cs[i + 2] = u.z; cs[i + 3] = u.w;
+        sn[i] = w.x; sn[i + 1] = w.y; sn[i + 2] = w.z; sn[i + 3] = w.w;
       }
     }
-    for (int h0 = g; h0 < heads; h0 += kRopeAhead * ng) {
-      uint4 x[kRopeAhead];
+    if constexpr (!kInterleaved) {
 #pragma unroll
-      for (int u = 0; u < kRopeAhead; ++u) {
-        const int h = h0 + u * ng;
-        if (h >= heads) continue;
-        const uint16_t* src = h < a.hq ? a.q + t * a.qs + int64_t(h) * d
-                            : h < a.hq + a.hkv ? a.k + t * a.ks + int64_t(h - a.hq) * d
-                                               : a.v + t * a.vs + int64_t(h - a.hq - a.hkv) * d;
-        x[u] = *reinterpret_cast<const uint4*>(src + 8 * c);
-      }
+      for (int i = 0; i < 8; ++i) sn[i] = second ? sn[i] : -sn[i];
+    }
+    for (int h0 = g; h0 < heads; h0 += kRopeAhead * ng) {
+      if (h0 != g) load(h0);
 #pragma unroll
       for (int u = 0; u < kRopeAhead; ++u) {
         const int h = h0 + u * ng;
         if (h >= heads) continue;
         if (h >= a.hq + a.hkv) {
           if (row >= 0)
-            *reinterpret_cast<uint2*>(a.v_cache + row + int64_t(h - a.hq - a.hkv) * d + 8 * c) =
+            *reinterpret_cast<uint2*>(a.v_cache + row + int64_t(h - a.hq - a.hkv) * kD + 8 * c) =
                 quant8<false>(x[u], a.v_scale, a.v_inv);
           continue;
         }
-        const uint16_t* w = h < a.hq ? a.qw : a.kw;
+        const bool isq = h < a.hq;
         float r = 1.0f;
-        uint4 wv = ones;
-        if (w) {
-          wv = *reinterpret_cast<const uint4*>(w + 8 * c);
-          float sq = sq_sum8(x[u]);
-#pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) sq += __shfl_xor(sq, o);
-          r = 1.0f / sqrtf(sq * (1.0f / float(8 * kLanes)) + a.eps);
-        }
-        float n[8], wf[8];
+        if (isq ? a.qw != nullptr : a.kw != nullptr)
+          r = rsqrtf(sum_over_lanes<kLanesLog2>(sq_sum8(x[u])) * (1.0f / float(kD)) + a.eps);
+        float n[8], w[8], y[8];
         unpack8(x[u], n);
-        unpack8(wv, wf);
+        unpack8(isq ? qw : kw, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) n[i] = n[i] * r * wf[i];
-        float y[8];
+        for (int i = 0; i < 8; ++i) n[i] = n[i] * r * w[i];
         if constexpr (kInterleaved) {
 #pragma unroll
           for (int i = 0; i < 8; i += 2) {
@@ -136,19 +172,23 @@ __global__ __launch_bounds__(1024) void rope_vec_kernel(const RopeArgs a) {
             y[i + 1] = turns ? n[i + 1] * cs[i / 2] + n[i] * sn[i / 2] : n[i + 1];
           }
         } else {
-          const int from = turns ? partner : c;
+          float o[8], wp[8];
+          const uint4 other = make_uint4(__shfl(x[u].x, partner, kLanes), __shfl(x[u].y, partner, kLanes),
+                                         __shfl(x[u].z, partner, kLanes), __shfl(x[u].w, partner, kLanes));
+          unpack8(other, o);
+          unpack8(isq ? qwp : kwp, wp);
+          // beyond the rotated part the value itself comes out: a product with 0 would turn an
+          // infinity into NaN
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float o = __shfl(n[i], from, kLanes);
-            y[i] = turns ? n[i] * cs[i] + (second ? o : -o) * sn[i] : n[i];
-          }
+          for (int i = 0; i < 8; ++i)
+            y[i] = turns ? n[i] * cs[i] + (o[i] * r * wp[i]) * sn[i] : n[i];
         }
         const uint4 out = make_uint4(cvt_bf16x2(y[0], y[1]), cvt_bf16x2(y[2], y[3]),
                                      cvt_bf16x2(y[4], y[5]), cvt_bf16x2(y[6], y[7]));
-        if (h < a.hq) {
-          *reinterpret_cast<uint4*>(a.q_out + t * a.qos + int64_t(h) * d + 8 * c) = out;
+        if (isq) {
+          *reinterpret_cast<uint4*>(a.q_out + t * a.qos + int64_t(h) * kD + 8 * c) = out;
         } else {
-          const int64_t at = int64_t(h - a.hq) * d + 8 * c;
+          const int64_t at = int64_t(h - a.hq) * kD + 8 * c;
           if (a.k_out) *reinterpret_cast<uint4*>(a.k_out + t * a.kos + at) = out;
           if (row >= 0)
             *reinterpret_cast<uint2*>(a.k_cache + row + at) =
@@ -200,7 +240,7 @@ __global__ __launch_bounds__(64 * kRopeRows) void rope_scalar_kernel(const RopeA
       }
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) sq += __shfl_xor(sq, o);
-      r = 1.0f / sqrtf(sq / float(a.d) + a.eps);
+      r = rsqrtf(sq / float(a.d) + a.eps);
     }
     auto normed = [&](int i) {
       const float f = bf16_to_f32(x[i]);
@@ -253,8 +293,11 @@ int rope_run(const RopeArgs& a, int interleaved, hipStream_t stream) {
            interleaved);
     return launch_status();
   }
+  // Few tokens: a lane group for every head of the token.  Many: 256 threads, so that a lane
+  // uses its cosines and weights for several heads.
   const int64_t want = (heads * lanes + 63) / 64 * 64;
-  const unsigned threads = unsigned(want < 256 ? want : 256);
+  const int64_t most = a.tokens <= 2 * num_cus() ? 1024 : 256;
+  const unsigned threads = unsigned(want < most ? want : most);
   const unsigned blocks = unsigned(clamp_grid(a.tokens));
   void (*kern)(RopeArgs) = nullptr;
   switch (lanes) {

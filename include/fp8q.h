@@ -51,7 +51,7 @@ int fp8q_version(void);
  * `start` as it begins executing and `stop` as it completes (hipExtLaunchKernelGGL), so
  * the events' elapsed time is that kernel's own duration.  Either may be NULL.  Every
  * entry point below enqueues exactly one kernel per call, except calls that enqueue
- * nothing (zero sizes, errors) and the calibrator.  Always returns FP8Q_OK. */
+ * nothing (zero sizes, errors), the calibrator and fp8_attn_decode.  Always returns FP8Q_OK. */
 int fp8q_time_next_launch(hipEvent_t start, hipEvent_t stop);
 
 /* Measurement references (not steps of the path): kernels that the path's timings are read
@@ -432,14 +432,13 @@ int attn_prefill(const uint16_t* q, const uint16_t* k, const uint16_t* v,
  *   block_tables      device int32 [num_seqs, table_stride], the first max_blocks of each row used
  *   context_lens      device int32 [num_seqs];  lse  device fp32 [num_seqs, num_q_heads] or NULL
  *   workspace   device memory of workspace_bytes >= fp8_attn_decode_workspace_size's, 256-byte
- *               aligned; its counts (the first ceil(num_seqs * Hkv * ceil(Hq / Hkv / 16) * 4 / 256)
- *               * 256 bytes) must be zero before the first call that uses it, e.g. all of it
- *               zero-filled at allocation, and every call leaves them zero; a call of another
- *               shape needs them zeroed up to its own size, which a zero-filled workspace used
- *               only for one shape always is.  Calls sharing a workspace must not overlap in time.
+ *               aligned, of any content (nothing is kept in it from call to call); calls that
+ *               share one must not overlap in time
  *   head_dim in {64, 128, 256}; num_q_heads a multiple of num_kv_heads; block_size > 0;
- *   max_blocks * block_size <= 2^30; cache_stride >= block_size*H*D, a multiple of 16; q / out
+ *   max_blocks * block_size <= 2^30 and num_seqs * (max_blocks * block_size / 32 + 1) <= 2^30;
+ *   cache_stride >= block_size*H*D, a multiple of 16; q / out
  *   strides multiples of 8; k_scale, v_scale in [2^-64, 2^64]; 0 < softmax_scale <= 2^32.
+ * Enqueues two kernels (the second joins the parts of long histories).
  * fp8_attn_decode_workspace_size: for the current device.
  * Errors: FP8Q_EINVAL, FP8Q_ENULL, FP8Q_EALIGN, FP8Q_ELAUNCH. */
 int fp8_attn_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,

@@ -110,8 +110,8 @@ def test_decode_workspace_size():
     for bad in [(-1, 8, 2, 128), (2, 7, 2, 128), (2, 8, 2, 100), (2, 8, 0, 128)]:
         assert lib.fp8_attn_decode_workspace_size(*bad, ctypes.byref(b)) == EINVAL
         assert b.value == 0
-    sizes = [fq.fp8_attn_decode_workspace_size(n, 40, 4, 128) for n in (0, 1, 16, 64)]
-    assert sizes[0] == 0 and sizes[1] < sizes[2] < sizes[3]
+    assert fq.fp8_attn_decode_workspace_size(0, 40, 4, 128) == 0
+    assert fq.fp8_attn_decode_workspace_size(1, 40, 4, 128) > 0
 
 
 # ------------------------------------------------------------------------- the binding

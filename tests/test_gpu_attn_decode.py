@@ -90,12 +90,11 @@ def test_head_groups(hq, hkv, d):
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_long_histories_split_over_workgroups(lens, d):
     s, out, lse = _run(lens, 8, 2, d, 16)
-    ws = torch.zeros(fq.fp8_attn_decode_workspace_size(len(lens), 8, 2, d), dtype=torch.uint8,
-                     device=DEV)
-    for _ in range(3):  # the same bits every time; counts back at zero
+    need = fq.fp8_attn_decode_workspace_size(len(lens), 8, 2, d)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV)  # any content will do
+    for _ in range(3):  # the same bits every time
         again = _call(s, workspace=ws)
         assert torch.equal(again, out)
-        assert not ws[:-(-len(lens) * 2 * 4 // 256) * 256].any()
 
 
 @pytest.mark.parametrize("seqs", [63, 64, 65, 130, 300])
