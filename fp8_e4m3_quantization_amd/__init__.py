@@ -15,6 +15,7 @@ from ._lib import (  # noqa: F401
     KvCalibrator,
     KvTarget,
     attn_prefill,
+    attn_prefill_workspace_size,
     fp8_attn_decode,
     fp8_attn_decode_workspace_size,
     fp8_block_quant,
@@ -28,7 +29,6 @@ from ._lib import (  # noqa: F401
     fp8_quant_w8a8_gemm_grouped,
     load,
     strerror,
-    attn_workspace,
     gemm_workspace,
     qk_norm_rope,
     w8a8_block_gemm,

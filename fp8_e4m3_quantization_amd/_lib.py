@@ -29,7 +29,7 @@ EXPORTS = (
     "fp8_quant_w8a8_gemm_grouped", "w8a16_block_gemv", "w8a16_block_gemv_grouped",
     "fp8_kv_write", "fp8_kv_write_amax", "fp8_kv_read", "fp8_kv_amax",
     "qk_norm_rope", "fp8_qk_norm_rope_kv_write", "attn_prefill",
-    "fp8_attn_decode_workspace_size", "fp8_attn_decode",
+    "attn_prefill_workspace_size", "fp8_attn_decode_workspace_size", "fp8_attn_decode",
     "fp8q_kv_calib_create", "fp8q_kv_calib_create_with_ops", "fp8q_kv_calib_observe",
     "fp8q_kv_calib_decide", "fp8q_kv_calib_scales", "fp8q_kv_calib_state",
     "fp8q_kv_calib_destroy",
@@ -141,7 +141,9 @@ def load() -> ctypes.CDLL:
                                                      P, I32, I32, I32, I32, I32, I64, F32, F32,
                                                      I64, I64, I64, I64, P, P, I64, I64, P]),
         "attn_prefill": (ctypes.c_int, [P, P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, F32,
-                                        I32, I64, I64, I64, I64, P]),
+                                        I32, I64, I64, I64, I64, P, ctypes.c_uint64, P]),
+        "attn_prefill_workspace_size": (ctypes.c_int, [I32, I32, I32, I32, I32, I32,
+                                                       ctypes.POINTER(ctypes.c_uint64)]),
         "fp8_attn_decode_workspace_size": (ctypes.c_int, [I32, I32, I32, I32,
                                                           ctypes.POINTER(ctypes.c_uint64)]),
         "fp8_attn_decode": (ctypes.c_int, [P, P, P, P, P, P, P, I32, I32, I64, I32, I32, I32, I32,
@@ -714,16 +716,60 @@ def _check_lse(lse, rows, heads):
         raise ValueError(f"lse must be [{rows}, {heads}]")
 
 
+_ATTN_SIZES = {}       # (entry point, device index, shape) -> its workspace size there
+_ATTN_WORKSPACES = {}  # (device index, stream) -> uint8 tensor
+
+
+def _workspace_size(fn: str, *shape) -> int:
+    b = ctypes.c_uint64()
+    check(fn, getattr(load(), fn)(*shape, ctypes.byref(b)))
+    return b.value
+
+
+def _attn_workspace(fn: str, index: int, stream, *shape):
+    """A workspace for a call of this shape on `stream` of GPU `index`, kept and reused by later
+    calls there; None where none is needed.  While a graph is being captured a new one is made
+    instead, in the graph's own memory, so that no two graphs share one."""
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _attn_workspace(fn, index, stream, *shape)
+    need = _ATTN_SIZES.get((fn, index, shape))
+    if need is None:
+        need = _ATTN_SIZES[(fn, index, shape)] = _workspace_size(fn, *shape)
+    if need == 0:
+        return None
+    if stream is not None and stream != torch._C._cuda_getCurrentRawStream(index):
+        with _on_stream(stream, torch.device("cuda", index)):
+            return _attn_workspace(fn, index, None, *shape)
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
+    key = (index, torch._C._cuda_getCurrentRawStream(index))
+    ws = _ATTN_WORKSPACES.get(key)
+    if ws is None or ws.numel() < need:
+        ws = _ATTN_WORKSPACES[key] = torch.empty(need, dtype=torch.uint8,
+                                                 device=torch.device("cuda", index))
+    return ws
+
+
+def attn_prefill_workspace_size(num_seqs: int, total_q: int, total_k: int, num_q_heads: int,
+                                num_kv_heads: int, head_dim: int) -> int:
+    """Bytes of workspace that attn_prefill needs for this shape on the current device (0: none)."""
+    return _workspace_size("attn_prefill_workspace_size", num_seqs, total_q, total_k, num_q_heads,
+                           num_kv_heads, head_dim)
+
+
 def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
                  num_q_heads: int, num_kv_heads: int, head_dim: int,
                  cu_seqlens_k: torch.Tensor | None = None, softmax_scale: float | None = None,
                  causal: bool = True, out: torch.Tensor | None = None,
-                 lse: torch.Tensor | None = None, stream: int | None = None) -> torch.Tensor:
+                 lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                 stream: int | None = None) -> torch.Tensor:
     """Attention over packed prompts: q [tokens, Hq * D], k / v [tokens, Hkv * D] bf16, int32
     cu_seqlens [num_seqs + 1] on the device (cu_seqlens_k: the queries' own when None; longer
     sequences of keys put the queries at their end).  softmax_scale: head_dim ** -0.5 when None.
     Rows outside every sequence are left as they were (zeros when allocated here); lse, if given,
-    is fp32 [tokens, Hq]."""
+    is fp32 [tokens, Hq].  workspace: uint8, attn_prefill_workspace_size's bytes, for one call at a
+    time; by default one kept per stream by this module."""
     tq, qs = _head_rows(q, "q", num_q_heads, head_dim)
     tk, ks = _head_rows(k, "k", num_kv_heads, head_dim)
     tv, vs = _head_rows(v, "v", num_kv_heads, head_dim)
@@ -741,53 +787,25 @@ def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q
         raise ValueError(f"out has {to} rows, q has {tq}")
     _check_lse(lse, tq, num_q_heads)
     i = _gpu_index(q, "q")
+    seqs = cu_seqlens_q.numel() - 1
+    if workspace is None:
+        workspace = _attn_workspace("attn_prefill_workspace_size", i, stream, seqs, tq, tk,
+                                    num_q_heads, num_kv_heads, head_dim)
     _call("attn_prefill", i, stream, _ptr(q, "q", _BF16S, i, False), _ptr(k, "k", _BF16S, i, False),
           _ptr(v, "v", _BF16S, i, False), _ptr(cu_seqlens_q, "cu_seqlens_q", _I32S, i),
           _ptr(cu_seqlens_k, "cu_seqlens_k", _I32S, i), _ptr(out, "out", _BF16S, i, False),
-          _ptr(lse, "lse", _F32S, i), cu_seqlens_q.numel() - 1, tq, tk, num_q_heads, num_kv_heads,
-          head_dim, head_dim ** -0.5 if softmax_scale is None else softmax_scale,
-          1 if causal else 0, qs, ks, vs, os_)
+          _ptr(lse, "lse", _F32S, i), seqs, tq, tk, num_q_heads, num_kv_heads, head_dim,
+          head_dim ** -0.5 if softmax_scale is None else softmax_scale, 1 if causal else 0, qs, ks,
+          vs, os_, _ptr(workspace, "workspace", _BYTES, i),
+          0 if workspace is None else workspace.numel())
     return out
 
 
 def fp8_attn_decode_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int,
                                    head_dim: int) -> int:
     """Bytes of workspace that fp8_attn_decode needs for this shape on the current device."""
-    b = ctypes.c_uint64()
-    check("fp8_attn_decode_workspace_size",
-          load().fp8_attn_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
-                                                ctypes.byref(b)))
-    return b.value
-
-
-_ATTN_SIZES = {}       # (device index, shape) -> fp8_attn_decode_workspace_size there
-_ATTN_WORKSPACES = {}  # (device index, stream) -> uint8 tensor
-
-
-def attn_workspace(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
-                   device: int | None = None, stream: int | None = None) -> torch.Tensor:
-    """A workspace for fp8_attn_decode calls of this shape on `stream`, kept and reused by its
-    later calls.  While a graph is being captured a new one is made instead, in the graph's own
-    memory, so that no two graphs share one."""
-    index = torch.cuda.current_device() if device is None else device
-    if torch.cuda.current_device() != index:
-        with torch.cuda.device(index):
-            return attn_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, index, stream)
-    if stream is not None and stream != torch._C._cuda_getCurrentRawStream(index):
-        with _on_stream(stream, torch.device("cuda", index)):
-            return attn_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, index)
-    shape = (index, num_seqs, num_q_heads, num_kv_heads, head_dim)
-    need = _ATTN_SIZES.get(shape)
-    if need is None:
-        need = _ATTN_SIZES[shape] = fp8_attn_decode_workspace_size(*shape[1:])
-    if torch.cuda.is_current_stream_capturing():
-        return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
-    key = (index, torch._C._cuda_getCurrentRawStream(index))
-    ws = _ATTN_WORKSPACES.get(key)
-    if ws is None or ws.numel() < need:
-        ws = _ATTN_WORKSPACES[key] = torch.empty(need, dtype=torch.uint8,
-                                                 device=torch.device("cuda", index))
-    return ws
+    return _workspace_size("fp8_attn_decode_workspace_size", num_seqs, num_q_heads, num_kv_heads,
+                           head_dim)
 
 
 def fp8_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -801,7 +819,7 @@ def fp8_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     block_tables [num_seqs, max_blocks] and context_lens [num_seqs] (the token's own position
     included, written before).  softmax_scale: head_dim ** -0.5 when None; lse, if given, is fp32
     [num_seqs, Hq].  workspace: uint8, fp8_attn_decode_workspace_size's bytes, for one call
-    at a time; by default attn_workspace's."""
+    at a time; by default one kept per stream by this module."""
     n, qs = _head_rows(q, "q", num_q_heads, head_dim)
     cs = block_size * num_kv_heads * head_dim if cache_stride is None else cache_stride
     blocks = _kv_num_blocks(k_cache, v_cache, cs)
@@ -821,7 +839,8 @@ def fp8_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     if n == 0:
         return out
     if workspace is None:
-        workspace = attn_workspace(n, num_q_heads, num_kv_heads, head_dim, i, stream)
+        workspace = _attn_workspace("fp8_attn_decode_workspace_size", i, stream, n, num_q_heads,
+                                    num_kv_heads, head_dim)
     _call("fp8_attn_decode", i, stream, _ptr(q, "q", _BF16S, i, False),
           _ptr(k_cache, "k_cache", _U8S, i), _ptr(v_cache, "v_cache", _U8S, i),
           _ptr(block_tables, "block_tables", _I32S, i, False),

@@ -29,6 +29,8 @@ namespace {
 
 constexpr int kTileKeys = 64;
 constexpr int kWaveRows = 32;
+constexpr int kPrefillWaves = 4;
+constexpr int kPrefillRows = kWaveRows * kPrefillWaves;  // queries of a workgroup
 constexpr int kOrderedSeqs = 256;  // batches up to this size run their longest tiles first
 
 struct PrefillArgs {
@@ -38,8 +40,18 @@ struct PrefillArgs {
   const int32_t *cu_q, *cu_k;
   int64_t qs, ks, vs, os;
   int seqs, tq, tk, hq, hkv, causal;
+  int items;         // work items there is room for
+  int most_parts;    // parts of a tile's keys; 1: not split
   float scale_log2;  // softmax scale * log2(e)
+  float* sums;       // [work items][parts][rows][D] where split
+  float2* stats;     // [work items][parts][rows]: reference (log2 units), sum of weights
 };
+
+// Parts that `tiles` tiles of keys are split into: no part is short.
+constexpr int kPartTiles = 8;
+__device__ __forceinline__ int parts_of(const PrefillArgs& a, int tiles) {
+  return max(min(a.most_parts, tiles / kPartTiles), 1);
+}
 
 // Start and length of sequence s among `total` rows, whatever the list holds.
 __device__ __forceinline__ void seq_span(const int32_t* cu, int s, int total, int* start, int* len) {
@@ -122,6 +134,40 @@ __device__ __forceinline__ bool find_tile(const PrefillArgs& a, int rows, int ra
   return false;
 }
 
+// A work item: a tile of queries of one head.  Workgroups go to the 8 XCDs in turn; where the
+// heads divide, each XCD takes neighbouring heads, which share keys and values in its L2.
+struct Item {
+  int head, seq, tile, q0, lq, kv0, lk;
+  // keys [0, seen(i)) are seen by query i
+  __device__ __forceinline__ int seen(const PrefillArgs& a, int i) const {
+    return a.causal ? min(max(i + lk - lq + 1, 0), lk) : lk;
+  }
+  // tiles of keys that some query of the tile sees
+  __device__ __forceinline__ int key_tiles(const PrefillArgs& a) const {
+    const int last = min((tile + 1) * kPrefillRows, lq) - 1;
+    return __builtin_amdgcn_readfirstlane((seen(a, last) + kTileKeys - 1) / kTileKeys);
+  }
+};
+__device__ __forceinline__ bool find_item(const PrefillArgs& a, int index, Item* it) {
+  if (index >= a.items) return false;
+  int rank;
+  if (a.hq % 8 == 0) {
+    const int per = a.hq / 8, i = index / 8;
+    it->head = (index % 8) * per + i % per;
+    rank = i / per;
+  } else {
+    it->head = index % a.hq;
+    rank = index / a.hq;
+  }
+  int seq, tile;
+  if (!find_tile(a, kPrefillRows, rank, &seq, &tile)) return false;
+  it->seq = __builtin_amdgcn_readfirstlane(seq);
+  it->tile = __builtin_amdgcn_readfirstlane(tile);
+  seq_span(a.cu_q, it->seq, a.tq, &it->q0, &it->lq);
+  seq_span(a.cu_k, it->seq, a.tk, &it->kv0, &it->lk);
+  return true;
+}
+
 // Order of the 16-byte chunks within a row of a tile in LDS.  K is read 16 rows at a time, one
 // chunk each; V (transposing read) four rows at a time, 64 bytes each: both then touch every bank
 // once.
@@ -143,9 +189,31 @@ __device__ __forceinline__ uint32_t non_finite(uint32_t w) {
   return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
 }
 
-template <int D, int kWaves>
+// The order of a turn of the pipeline below: the score products with the previous tile's weights
+// between them, each K read two steps ahead of its product, then the value products.
+template <int D>
+__device__ __forceinline__ void pair_up() {
+  constexpr int kMfma = 0x008, kVector = 0x002, kLdsRead = 0x100;
+  __builtin_amdgcn_sched_group_barrier(kLdsRead, 6, 0);
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(kVector, 6, 0);
+    __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(kVector, 6, 0);
+    __builtin_amdgcn_sched_group_barrier(kLdsRead, 2, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(kLdsRead, 2, 0);
+    __builtin_amdgcn_sched_group_barrier(kVector, 2, 0);
+  }
+}
+
+template <int D>
 __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
-  constexpr int kRows = kWaveRows * kWaves;
+  constexpr int kWaves = kPrefillWaves;
   constexpr int kChunks = D / 8;                              // 16-byte chunks of a row
   constexpr int kCopies = kTileKeys * kChunks / (64 * kWaves);  // 1 KB copies per wave and tile
   __shared__ __attribute__((aligned(16))) uint16_t k0[kTileKeys * D], k1[kTileKeys * D];
@@ -153,35 +221,29 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
   const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-  // heads: workgroups go to the 8 XCDs in turn; where the heads divide, each XCD takes
-  // neighbouring heads (which share keys and values in its L2)
-  int head, rank;
-  if (a.hq % 8 == 0) {
-    const int per = a.hq / 8, i = blockIdx.x / 8;
-    head = (blockIdx.x % 8) * per + i % per;
-    rank = i / per;
-  } else {
-    head = blockIdx.x % a.hq;
-    rank = blockIdx.x / a.hq;
-  }
-  int seq, tile;
-  if (!find_tile(a, kRows, rank, &seq, &tile)) return;
-  seq = __builtin_amdgcn_readfirstlane(seq);
-  tile = __builtin_amdgcn_readfirstlane(tile);
-  int q0, lq, kv0, lk;
-  seq_span(a.cu_q, seq, a.tq, &q0, &lq);
-  seq_span(a.cu_k, seq, a.tk, &kv0, &lk);
-  const int kvh = head / (a.hq / a.hkv);
-  const int first = tile * kRows;                    // the workgroup's first query
+  // (an item's parts lie 8 apart, on one XCD, where the heads are spread over them)
+  const int index = a.most_parts == 1 ? blockIdx.x
+                    : blockIdx.x / (8 * a.most_parts) * 8 + blockIdx.x % 8;
+  const int part = a.most_parts == 1 ? 0 : blockIdx.x / 8 % a.most_parts;
+  Item it;
+  if (!find_item(a, index, &it)) return;
+  const int head = it.head, q0 = it.q0, lq = it.lq, kvh = head / (a.hq / a.hkv);
+  const int first = it.tile * kPrefillRows;          // the workgroup's first query
   const int mine = first + wave * kWaveRows;         // this wave's
-  // keys [0, seen(i)) are seen by query i
-  auto seen = [&](int i) { return a.causal ? min(max(i + lk - lq + 1, 0), lk) : lk; };
-  const int last = min(first + kRows, lq) - 1;
-  const int tiles = (seen(last) + kTileKeys - 1) / kTileKeys;
-  const int row = mine + col;                        // this lane's query
+  const int row = mine + col;                        // this lane's
+  const int all_tiles = it.key_tiles(a), parts = parts_of(a, all_tiles);
+  if (part >= parts) return;
+  // this part's keys: rows kv0 .. kv0 + lk - 1 of k and v, in `tiles` tiles
+  const int from_tile = all_tiles * part / parts, from = from_tile * kTileKeys;
+  const int tiles = all_tiles * (part + 1) / parts - from_tile;
+  const int kv0 = it.kv0 + from, lk = min(it.lk - from, tiles * kTileKeys);
+  auto seen = [&](int i) { return min(max(it.seen(a, i) - from, 0), lk); };
   const int limit = row < lq ? seen(row) : 0;
-  const int wave_limit = mine < lq ? seen(min(mine + kWaveRows, lq) - 1) : 0;
-  const int all_see = seen(first);                   // every query of the workgroup sees these
+  const int wave_limit =
+      __builtin_amdgcn_readfirstlane(mine < lq ? seen(min(mine + kWaveRows, lq) - 1) : 0);
+  // tiles that every query of the workgroup sees whole: an odd number, or none
+  const int sees_all = __builtin_amdgcn_readfirstlane(seen(first) / kTileKeys);
+  const int whole = sees_all - (sees_all > 0 && sees_all % 2 == 0);
 
   v8bf qf[D / 16];
   {
@@ -191,31 +253,52 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
       qf[s] = __builtin_bit_cast(v8bf, *reinterpret_cast<const uint4*>(src + 16 * s));
   }
 
-  const uint16_t* kbase = a.k + int64_t(kv0) * a.ks + int64_t(kvh) * D;
-  const uint16_t* vbase = a.v + int64_t(kv0) * a.vs + int64_t(kvh) * D;
-  // The copy j of a wave fills 1 KB of the tile; the lane's place in it fixes the row and, by
-  // the chunk order, the chunk that it fetches.  Rows behind the last key fetch the last key.
-  auto copy_tile = [&](int t, uint16_t* dk, uint16_t* dv) {
-    const int left = lk - t * kTileKeys;  // > 0
-    const int span = min(left, kTileKeys);
-    const __amdgpu_buffer_rsrc_t rk = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint16_t*>(kbase + int64_t(t) * kTileKeys * a.ks), 0,
-        int(((span - 1) * a.ks + D) * 2), 0x00020000);
-    const __amdgpu_buffer_rsrc_t rv = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint16_t*>(vbase + int64_t(t) * kTileKeys * a.vs), 0,
-        int(((span - 1) * a.vs + D) * 2), 0x00020000);
+  // Copies of tiles, in order: copy j of a wave fills 1 KB of the tile; the lane's place in it fixes
+  // the row and, by the chunk order, the chunk that it fetches.  Rows behind the last key fetch
+  // the last key.
+  struct Source {
+    const uint16_t* at;  // the next tile's first row
+    int64_t tile;        // values from tile to tile
+    int step;            // bytes from row to row
+    int left;            // rows from the next tile on
+    int off[kCopies];
+  };
+  auto source = [&](const uint16_t* p, int64_t stride, auto chunk_of) {
+    Source c;
+    c.at = p + int64_t(kv0) * stride + int64_t(kvh) * D;
+    c.tile = kTileKeys * stride;
+    c.step = int(stride) * 2;
+    c.left = lk;
 #pragma unroll
     for (int j = 0; j < kCopies; ++j) {
-      const int at = (wave + kWaves * j) * 64 + lane;
-      const int r = at / kChunks, c = at % kChunks;
-      const int from = min(r, span - 1);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rk, (lds_void*)(dk + (wave + kWaves * j) * 512), 16,
-          int(from * a.ks * 2) + k_chunk<D>(r, c) * 16, 0, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rv, (lds_void*)(dv + (wave + kWaves * j) * 512), 16,
-          int(from * a.vs * 2) + v_chunk<D>(r, c) * 16, 0, 0, 0);
+      const int at = (wave + kWaves * j) * 64 + lane, r = at / kChunks;
+      c.off[j] = r * c.step + chunk_of(r, at % kChunks) * 16;
     }
+    return c;
+  };
+  Source ksrc = source(a.k, a.ks, [](int r, int c) { return k_chunk<D>(r, c); });
+  Source vsrc = source(a.v, a.vs, [](int r, int c) { return v_chunk<D>(r, c); });
+  auto copy_next = [&](Source& c, uint16_t* to) {
+    if (c.left <= 0) return;
+    const __amdgpu_buffer_rsrc_t from =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(c.at), 0, 0x7FFFFFFF, 0x00020000);
+    int w = wave;
+    asm volatile("" : "+s"(w));  // addresses in LDS are made here, not kept over the loop
+    if (c.left >= kTileKeys) {
+#pragma unroll
+      for (int j = 0; j < kCopies; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_void*)(to + (w + kWaves * j) * 512), 16,
+                                                 c.off[j], 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kCopies; ++j) {
+        const int behind = max(((wave + kWaves * j) * 64 + lane) / kChunks - c.left + 1, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_void*)(to + (w + kWaves * j) * 512), 16,
+                                                 c.off[j] - behind * c.step, 0, 0, 0);
+      }
+    }
+    c.at += c.tile;
+    c.left -= kTileKeys;
   };
 
   v16f o[D / 32];
@@ -223,38 +306,36 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
   for (int i = 0; i < D / 32; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
+  const float scale = a.scale_log2;
   float ref = neg_inf(), sum = 0.0f;  // reference (log2 units) and this half's weights
 
-  // S^T of tile t, softmax, O^T: kMasked tiles hold keys that some query does not see
-  auto compute = [&](int t, const uint16_t* kt, const uint16_t* vt, auto masked, bool odd_values) {
-    constexpr bool kMasked = decltype(masked)::value;
-    v16f s[2];
+  // S^T of a tile.
+  auto products = [&](v16f* s, const uint16_t* kt) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int r = 0; r < 16; ++r) s[b][r] = 0.0f;
 #pragma unroll
-      for (int st = 0; st < D / 16; ++st) {
+    for (int st = 0; st < D / 16; ++st)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
         const int r = 32 * b + col;
         const v8bf kf = __builtin_bit_cast(
             v8bf, *reinterpret_cast<const uint4*>(kt + r * D + k_chunk<D>(r, 2 * st + half) * 8));
         s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[st], s[b], 0, 0, 0);
       }
-    }
+  };
+  auto largest = [&](const v16f* s) {
     float top = neg_inf();
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        if (kMasked) {
-          const int key = t * kTileKeys + 32 * b + 8 * (r >> 2) + 4 * half + (r & 3);
-          s[b][r] = key < limit ? s[b][r] : neg_inf();
-        }
-        top = fmaxf(top, s[b][r]);
-      }
-    top = max_over_halves(top) * a.scale_log2;
-    if (__any(top > ref + kSoftmaxSlack)) {
-      const bool moves = top > ref + kSoftmaxSlack;
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
+    return max_over_halves(top) * scale;
+  };
+  auto move_to = [&](float top) {
+    const bool moves = top > ref + kSoftmaxSlack;
+    if (__any(moves)) {
       const float f = moves ? __builtin_amdgcn_exp2f(ref - top) : 1.0f;
       ref = moves ? top : ref;
       sum *= f;
@@ -263,58 +344,38 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[i][r] *= f;
     }
-    const float base = ref == neg_inf() ? 0.0f : ref;
-    v8bf p[4];
+  };
+  // Weights of 16 keys (step st of the tile) as the second product's operand.
+  auto weights = [&](const v16f* s, int st, float base) {
+    uint32_t w[4];
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int r = 0; r < 16; r += 8) {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][r + e], a.scale_log2, -base));
-          const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][r + e + 1], a.scale_log2, -base));
-          sum += x + y;
-          w[e / 2] = cvt_bf16x2(x, y);
-        }
-        p[2 * b + r / 8] = __builtin_bit_cast(v8bf, make_uint4(w[0], w[1], w[2], w[3]));
-      }
+    for (int e = 0; e < 8; e += 2) {
+      const int r = 8 * (st & 1) + e;
+      const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[st >> 1][r], scale, -base));
+      const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[st >> 1][r + 1], scale, -base));
+      sum += x + y;
+      w[e / 2] = cvt_bf16x2(x, y);
+    }
+    return __builtin_bit_cast(v8bf, v4u{w[0], w[1], w[2], w[3]});
+  };
+  // O^T += V^T P^T over 16 keys.
+  auto add_values = [&](const uint16_t* vt, int st, v8bf p) {
     const int i16 = lane & 15, side = (lane >> 4) & 1;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-      for (int st = 0; st < 4; ++st) {
-        const int ra = 16 * st + 4 * half + (i16 >> 2), c = 4 * i + 2 * side + ((i16 & 3) >> 1);
-        const int byte8 = 4 * (i16 & 1);  // elements into the chunk
-        const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (lds_v4s*)(vt + ra * D + v_chunk<D>(ra, c) * 8 + byte8));
-        const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (lds_v4s*)(vt + (ra + 8) * D + v_chunk<D>(ra + 8, c) * 8 + byte8));
-        v2u l2 = __builtin_bit_cast(v2u, lo), h2 = __builtin_bit_cast(v2u, hi);
-        v4u w = {l2[0], l2[1], h2[0], h2[1]};
-        if (kMasked && odd_values) {  // a masked weight of 0 times an infinity is not 0
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t bad = non_finite(w[e]);
-            w[e] &= ~((bad >> 15) * 0xFFFFu);
-          }
-        }
-        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, w), p[st], o[i], 0, 0, 0);
-      }
-    if (kMasked && odd_values) {  // the infinities and NaNs that this lane's query does see
-      for (int j = 0; j < kTileKeys; ++j)
-        if (t * kTileKeys + j < limit) {
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              const int e = 32 * i + 8 * (r >> 2) + 4 * half + (r & 3);
-              const uint32_t x = vt[j * D + v_chunk<D>(j, e >> 3) * 8 + (e & 7)];
-              if (non_finite(x)) o[i][r] += __uint_as_float(x << 16);
-            }
-        }
+    for (int i = 0; i < D / 32; ++i) {
+      const int ra = 16 * st + 4 * half + (i16 >> 2), c = 4 * i + 2 * side + ((i16 & 3) >> 1);
+      const int within = 4 * (i16 & 1);
+      const v2u lo = __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_v4s*)(vt + ra * D + v_chunk<D>(ra, c) * 8 + within)));
+      const v2u hi = __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_v4s*)(vt + (ra + 8) * D + v_chunk<D>(ra + 8, c) * 8 + within)));
+      o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, v4u{lo[0], lo[1], hi[0], hi[1]}),
+                                                     p, o[i], 0, 0, 0);
     }
   };
+  // A tile that some query does not see whole may hold infinities or NaNs where it does not look,
+  // and a weight of 0 times those is not 0.  They are rare: a tile that has any has them added,
+  // key by key, to the queries that see them, and zeroed in LDS before the products.
   auto odd_in = [&](const uint16_t* vt) {
     uint32_t any = 0;
 #pragma unroll
@@ -324,25 +385,108 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
     }
     return __syncthreads_or(any != 0) != 0;
   };
-  auto turn = [&](int t, const uint16_t* kt, const uint16_t* vt, uint16_t* kn, uint16_t* vn) {
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's copies of tile t landed
-    __syncthreads();                     // every wave's have, and the other buffers are free
-    if (t + 1 < tiles) copy_tile(t + 1, kn, vn);
-    if ((t + 1) * kTileKeys > all_see) {
-      const bool odd = odd_in(vt);
-      if (t * kTileKeys < wave_limit) compute(t, kt, vt, std::true_type{}, odd);
-    } else {
-      compute(t, kt, vt, std::false_type{}, false);
-    }
+  auto take_odd = [&](int t, uint16_t* vt) {
+    for (int j = 0; j < kTileKeys; ++j)
+      if (t * kTileKeys + j < limit) {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int e = 32 * i + 8 * (r >> 2) + 4 * half + (r & 3);
+            const uint32_t x = vt[j * D + v_chunk<D>(j, e >> 3) * 8 + (e & 7)];
+            if (non_finite(x)) o[i][r] += __uint_as_float(x << 16);
+          }
+      }
+    __syncthreads();
+    for (int j = threadIdx.x; j < kTileKeys * D; j += 64 * kWaves)
+      if (non_finite(vt[j])) vt[j] = 0;
+    __syncthreads();
   };
-  if (tiles > 0) copy_tile(0, k0, v0);
-  for (int t = 0; t < tiles; t += 2) {
-    turn(t, k0, v0, k1, v1);
-    if (t + 1 < tiles) turn(t + 1, k1, v1, k0, v0);
+  auto landed = [&]() {
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's copies landed
+    __syncthreads();                     // every wave's have, and the other buffers are free
+  };
+  // One turn of the pipeline: the scores of tile t + 1 (matrix cores) beside the weights of tile t
+  // (vector ALUs), then tile t's values (matrix cores) beside the largest of the new scores.
+  auto turn = [&](int t, const v16f* s, v16f* next, const uint16_t* kn, const uint16_t* vt,
+                  uint16_t* k_free, uint16_t* v_free) {
+    landed();
+    copy_next(ksrc, k_free);
+    copy_next(vsrc, v_free);
+    const float base = ref == neg_inf() ? 0.0f : ref;
+    products(next, kn);
+    v8bf p[4];
+#pragma unroll
+    for (int st = 0; st < 4; ++st) p[st] = weights(s, st, base);
+#pragma unroll
+    for (int st = 0; st < 4; ++st) add_values(vt, st, p[st]);
+    const float top = largest(next);
+    pair_up<D>();
+    move_to(top);
+  };
+  v16f sa[2];
+  int t = 0;
+  if (whole > 0) {
+    v16f sb[2];
+    copy_next(ksrc, k0);
+    landed();
+    copy_next(ksrc, k1);
+    copy_next(vsrc, v0);
+    products(sa, k0);
+    move_to(largest(sa));
+    for (; t + 1 < whole; t += 2) {
+      turn(t, sa, sb, k1, v0, k0, v1);
+      turn(t + 1, sb, sa, k0, v1, k1, v0);
+    }
+    landed();
+    copy_next(vsrc, v1);
+    const float base = ref == neg_inf() ? 0.0f : ref;
+#pragma unroll
+    for (int st = 0; st < 4; ++st) add_values(v0, st, weights(sa, st, base));
+    ++t;
+  } else if (tiles > 0) {
+    copy_next(ksrc, k0);
+    copy_next(vsrc, v0);
+  }
+  for (; t < tiles; ++t) {
+    uint16_t *kt = t & 1 ? k1 : k0, *vt = t & 1 ? v1 : v0;
+    landed();
+    copy_next(ksrc, t & 1 ? k0 : k1);
+    copy_next(vsrc, t & 1 ? v0 : v1);
+    const bool odd = odd_in(vt), mine_too = t * kTileKeys < wave_limit;
+    if (mine_too) {
+      const int left = limit - t * kTileKeys - 4 * half;
+      products(sa, kt);
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          sa[b][r] = 32 * b + 8 * (r >> 2) + (r & 3) < left ? sa[b][r] : neg_inf();
+          if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // few conditions alive at a time
+        }
+      move_to(largest(sa));
+    }
+    if (odd) take_odd(t, vt);
+    if (mine_too) {
+      const float base = ref == neg_inf() ? 0.0f : ref;
+#pragma unroll
+      for (int st = 0; st < 4; ++st) add_values(vt, st, weights(sa, st, base));
+    }
   }
 
   const float total = sum_over_halves(sum);
   if (row >= lq) return;
+  if (parts > 1) {
+    const int64_t at = (int64_t(index) * a.most_parts + part) * kPrefillRows + wave * kWaveRows + col;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; r += 4)
+        *reinterpret_cast<float4*>(a.sums + at * D + 32 * i + 2 * r + 4 * half) =
+            make_float4(o[i][r], o[i][r + 1], o[i][r + 2], o[i][r + 3]);
+    if (half == 0) a.stats[at] = make_float2(ref, total);
+    return;
+  }
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   uint16_t* dst = a.out + int64_t(q0 + row) * a.os + int64_t(head) * D + 4 * half;
 #pragma unroll
@@ -357,9 +501,82 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
         total == 0.0f ? neg_inf() : (ref + __builtin_amdgcn_logf(total)) * kLn2;
 }
 
-template <int D, int kWaves>
-__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void prefill_kernel(const PrefillArgs a) {
-  prefill_tile<D, kWaves>(a);
+template <int D>
+__global__ __launch_bounds__(64 * kPrefillWaves, D == 256 ? 1 : 2) void prefill_kernel(const PrefillArgs a) {
+  prefill_tile<D>(a);
+}
+
+// Adds up the parts of a work item's queries in order: a D/4-lane group per query at a time.
+constexpr int kPrefillJoinThreads = 256;
+template <int D>
+__global__ __launch_bounds__(kPrefillJoinThreads) void prefill_join_kernel(const PrefillArgs a) {
+  constexpr int kLanes = D / 4, kGroups = kPrefillJoinThreads / kLanes, kSplits = kPrefillRows / 32;
+  const int index = blockIdx.x / kSplits;
+  Item it;
+  if (!find_item(a, index, &it)) return;
+  const int parts = parts_of(a, it.key_tiles(a));
+  if (parts == 1) return;
+  const int first = blockIdx.x % kSplits * 32, d = threadIdx.x % kLanes * 4;
+  for (int r = first + int(threadIdx.x) / kLanes; r < first + 32; r += kGroups) {
+    const int row = it.tile * kPrefillRows + r;
+    if (row >= it.lq) return;
+    float ref = neg_inf(), total = 0.0f;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) {
+      const int64_t at = (int64_t(index) * a.most_parts + p) * kPrefillRows + r;
+      const float4 x = *reinterpret_cast<const float4*>(a.sums + at * D + d);
+      const float2 st = a.stats[at];
+      const float to = fmaxf(ref, st.x);
+      const float f = ref == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(ref - to);
+      const float h = st.x == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(st.x - to);
+      ref = to;
+      total = total * f + st.y * h;
+      v.x = v.x * f + x.x * h; v.y = v.y * f + x.y * h;
+      v.z = v.z * f + x.z * h; v.w = v.w * f + x.w * h;
+    }
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    *reinterpret_cast<uint2*>(a.out + int64_t(it.q0 + row) * a.os + int64_t(it.head) * D + d) =
+        make_uint2(cvt_bf16x2(v.x * inv, v.y * inv), cvt_bf16x2(v.z * inv, v.w * inv));
+    if (a.lse && d == 0)
+      a.lse[int64_t(it.q0 + row) * a.hq + it.head] =
+          total == 0.0f ? neg_inf() : (ref + __builtin_amdgcn_logf(total)) * kLn2;
+  }
+}
+
+// Work items of a call (an upper bound: tiles of whole sequences), and the parts that their keys
+// are split into: where the items leave half of the device idle and the keys are long, as many
+// as fill it.
+struct PrefillPlan {
+  int64_t items;
+  int parts;
+  uint64_t sums_bytes, bytes;
+};
+PrefillPlan prefill_plan(int32_t seqs, int32_t total_q, int32_t total_k, int32_t hq, int32_t d) {
+  PrefillPlan p = {};
+  p.items = (int64_t(total_q) / kPrefillRows + seqs) * hq;
+  const int64_t slots = (d == 256 ? 1 : 2) * int64_t(num_cus());
+  const int64_t by_items = slots / p.items;
+  const int64_t by_keys = int64_t(total_k) / seqs / (kTileKeys * kPartTiles);
+  p.parts = int(by_items < by_keys ? by_items : by_keys);
+  if (p.parts < 2) {
+    p.parts = 1;
+    return p;
+  }
+  if (p.parts > 64) p.parts = 64;
+  const uint64_t rows = uint64_t(p.items) * p.parts * kPrefillRows;
+  p.sums_bytes = rows * d * 4;
+  p.bytes = p.sums_bytes + rows * 8;
+  return p;
+}
+
+int prefill_shape(int32_t seqs, int32_t total_q, int32_t total_k, int32_t hq, int32_t hkv, int32_t d) {
+  if (seqs < 0 || total_q < 0 || total_k < 0 || total_q > (1 << 30) || total_k > (1 << 30) ||
+      seqs > (1 << 24))
+    return FP8Q_EINVAL;
+  if (hq <= 0 || hkv <= 0 || hq % hkv != 0 || hq > 65536) return FP8Q_EINVAL;
+  if (d != 64 && d != 128 && d != 256) return FP8Q_EINVAL;
+  return FP8Q_OK;
 }
 
 }  // namespace
@@ -367,20 +584,27 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void prefill_kernel(
 
 using namespace fp8q;
 
+extern "C" int attn_prefill_workspace_size(int32_t num_seqs, int32_t total_q, int32_t total_k,
+                                           int32_t num_q_heads, int32_t num_kv_heads,
+                                           int32_t head_dim, uint64_t* bytes) {
+  if (!bytes) return FP8Q_ENULL;
+  *bytes = 0;
+  const int rc = prefill_shape(num_seqs, total_q, total_k, num_q_heads, num_kv_heads, head_dim);
+  if (rc != FP8Q_OK) return rc;
+  if (num_seqs > 0 && total_q > 0)
+    *bytes = prefill_plan(num_seqs, total_q, total_k, num_q_heads, head_dim).bytes;
+  return FP8Q_OK;
+}
+
 extern "C" int attn_prefill(const uint16_t* q, const uint16_t* k, const uint16_t* v,
                             const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, uint16_t* out,
                             float* lse, int32_t num_seqs, int32_t total_q, int32_t total_k,
                             int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                             float softmax_scale, int32_t causal, int64_t q_stride,
                             int64_t key_stride, int64_t value_stride, int64_t out_stride,
-                            hipStream_t stream) {
-  if (num_seqs < 0 || total_q < 0 || total_k < 0 || total_q > (1 << 30) || total_k > (1 << 30) ||
-      num_seqs > (1 << 24))
-    return FP8Q_EINVAL;
-  if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
-      num_q_heads > 65536)
-    return FP8Q_EINVAL;
-  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return FP8Q_EINVAL;
+                            void* workspace, uint64_t workspace_bytes, hipStream_t stream) {
+  const int rc = prefill_shape(num_seqs, total_q, total_k, num_q_heads, num_kv_heads, head_dim);
+  if (rc != FP8Q_OK) return rc;
   if (!(softmax_scale > 0.0f && softmax_scale <= 0x1p64f)) return FP8Q_EINVAL;
   const int64_t eq = int64_t(num_q_heads) * head_dim, ek = int64_t(num_kv_heads) * head_dim;
   const int64_t most = int64_t(1) << 23;  // a tile's 64 rows stay within 32-bit byte offsets
@@ -393,18 +617,29 @@ extern "C" int attn_prefill(const uint16_t* q, const uint16_t* k, const uint16_t
       !aligned(lse, 4) || !aligned(cu_seqlens_q, 4) || !aligned(cu_seqlens_k, 4) ||
       q_stride % 8 || key_stride % 8 || value_stride % 8 || out_stride % 8)
     return FP8Q_EALIGN;
+  const PrefillPlan p = prefill_plan(num_seqs, total_q, total_k, num_q_heads, head_dim);
+  if (p.bytes > 0) {
+    if (!workspace) return FP8Q_ENULL;
+    if (!aligned(workspace, 256)) return FP8Q_EALIGN;
+    if (workspace_bytes < p.bytes) return FP8Q_EINVAL;
+  }
   PrefillArgs a = {};
   a.q = q, a.k = k, a.v = v, a.out = out, a.lse = lse, a.cu_q = cu_seqlens_q;
   a.cu_k = cu_seqlens_k, a.qs = q_stride, a.ks = key_stride, a.vs = value_stride;
   a.os = out_stride, a.seqs = num_seqs, a.tq = total_q, a.tk = total_k, a.hq = num_q_heads;
   a.hkv = num_kv_heads, a.causal = causal != 0, a.scale_log2 = softmax_scale * kLog2e;
-  constexpr int kWaves = 4;
-  // tiles of whole sequences never exceed this many
-  const int64_t tiles = int64_t(total_q) / (kWaveRows * kWaves) + num_seqs;
-  const int64_t blocks = tiles * num_q_heads;
-  if (blocks > 0x7FFFFFFF) return FP8Q_EINVAL;
-  auto kern = head_dim == 64 ? prefill_kernel<64, kWaves>
-            : head_dim == 128 ? prefill_kernel<128, kWaves> : prefill_kernel<256, kWaves>;
-  launch(kern, dim3(unsigned(blocks)), dim3(64 * kWaves), 0, stream, a);
+  a.most_parts = p.parts, a.items = int(p.items);
+  a.sums = static_cast<float*>(workspace);
+  a.stats = p.bytes ? reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.sums_bytes) : nullptr;
+  // parts of an item lie 8 workgroups apart: whole eights of items
+  const int64_t blocks = p.parts == 1 ? p.items : (p.items + 7) / 8 * 8 * p.parts;
+  const int64_t joins = p.items * (kPrefillRows / 32);
+  if (p.items > 0x7FFFFFFF || blocks > 0x7FFFFFFF || joins > 0x7FFFFFFF) return FP8Q_EINVAL;
+  auto kern = head_dim == 64 ? prefill_kernel<64> : head_dim == 128 ? prefill_kernel<128> : prefill_kernel<256>;
+  launch(kern, dim3(unsigned(blocks)), dim3(64 * kPrefillWaves), 0, stream, a);
+  if (launch_status() != FP8Q_OK || p.parts == 1) return launch_status();
+  auto join = head_dim == 64 ? prefill_join_kernel<64>
+              : head_dim == 128 ? prefill_join_kernel<128> : prefill_join_kernel<256>;
+  launch(join, dim3(unsigned(joins)), dim3(kPrefillJoinThreads), 0, stream, a);
   return launch_status();
 }

@@ -51,7 +51,8 @@ int fp8q_version(void);
  * `start` as it begins executing and `stop` as it completes (hipExtLaunchKernelGGL), so
  * the events' elapsed time is that kernel's own duration.  Either may be NULL.  Every
  * entry point below enqueues exactly one kernel per call, except calls that enqueue
- * nothing (zero sizes, errors), the calibrator and fp8_attn_decode.  Always returns FP8Q_OK. */
+ * nothing (zero sizes, errors), the calibrator, attn_prefill and fp8_attn_decode (whose
+ * first kernel is the timed one).  Always returns FP8Q_OK. */
 int fp8q_time_next_launch(hipEvent_t start, hipEvent_t stop);
 
 /* Measurement references (not steps of the path): kernels that the path's timings are read
@@ -405,13 +406,23 @@ int fp8_qk_norm_rope_kv_write(const uint16_t* q, const uint16_t* k, const uint16
  *             total_k (the rows of q and of k); entries are clamped to that range
  *   head_dim in {64, 128, 256}; num_q_heads a multiple of num_kv_heads; strides multiples of 8,
  *   at most 2^23; total_q, total_k <= 2^30; 0 < softmax_scale <= 2^64.
+ *   workspace   device memory of workspace_bytes >= attn_prefill_workspace_size's, 256-byte
+ *               aligned, of any content (nothing is kept in it from call to call); calls that
+ *               share one must not overlap in time; NULL is fine where the size is 0
+ * Few queries over long keys are split along the keys: then two kernels are enqueued, the second
+ * joining the parts in order, and a workspace is needed (results do not depend on the order in
+ * which workgroups run).  attn_prefill_workspace_size: for the current device.
  * Errors: FP8Q_EINVAL, FP8Q_ENULL, FP8Q_EALIGN, FP8Q_ELAUNCH. */
+int attn_prefill_workspace_size(int32_t num_seqs, int32_t total_q, int32_t total_k,
+                                int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                uint64_t* bytes);
 int attn_prefill(const uint16_t* q, const uint16_t* k, const uint16_t* v,
                  const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, uint16_t* out,
                  float* lse, int32_t num_seqs, int32_t total_q, int32_t total_k,
                  int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                  float softmax_scale, int32_t causal, int64_t q_stride, int64_t key_stride,
-                 int64_t value_stride, int64_t out_stride, hipStream_t stream);
+                 int64_t value_stride, int64_t out_stride, void* workspace,
+                 uint64_t workspace_bytes, hipStream_t stream);
 
 /* ------------------------------- single-token attention over the paged E4M3 cache
  * [staging] module doc: paged attention reads a sequence's whole history at the one scale the

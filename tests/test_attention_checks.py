@@ -54,11 +54,12 @@ def test_norm_rope_write_refusals():
 
 def _prefill(**over):
     a = dict(q=FAKE, k=FAKE, v=FAKE, cq=FAKE, ck=FAKE, out=FAKE, lse=FAKE, n=2, tq=64, tk=64, hq=8,
-             hkv=2, d=128, scale=0.1, causal=1, qs=1024, ks=256, vs=256, os=1024)
+             hkv=2, d=128, scale=0.1, causal=1, qs=1024, ks=256, vs=256, os=1024, ws=None, wb=0)
     a.update(over)
     return fq.load().attn_prefill(*[a[x] for x in ("q", "k", "v", "cq", "ck", "out", "lse", "n", "tq",
                                                    "tk", "hq", "hkv", "d", "scale", "causal", "qs",
-                                                   "ks", "vs", "os")], None)
+                                                   "ks", "vs", "os", "ws", "wb")],
+                                    None)
 
 
 def test_prefill_refusals():
@@ -75,6 +76,18 @@ def test_prefill_refusals():
         assert _prefill(**over) == EALIGN, over
     assert _prefill(n=0, q=None) == 0
     assert _prefill(tq=0, q=None) == 0
+    split = dict(n=1, tq=64, tk=100000)  # few queries over long keys: a workspace is needed
+    need = fq.attn_prefill_workspace_size(1, 64, 100000, 8, 2, 128)
+    assert need > 0 and fq.attn_prefill_workspace_size(1, 100000, 100000, 8, 2, 128) == 0
+    assert _prefill(**split) == ENULL
+    assert _prefill(**split, ws=FAKE, wb=need - 1) == EINVAL
+    assert _prefill(**split, ws=FAKE + 16, wb=need) == EALIGN
+    b = ctypes.c_uint64(7)
+    lib = fq.load()
+    assert lib.attn_prefill_workspace_size(1, 64, 64, 8, 2, 128, None) == ENULL
+    for bad in [(-1, 64, 64, 8, 2, 128), (1, -1, 64, 8, 2, 128), (1, 64, 64, 8, 3, 128),
+                (1, 64, 64, 8, 2, 96)]:
+        assert lib.attn_prefill_workspace_size(*bad, ctypes.byref(b)) == EINVAL and b.value == 0
 
 
 def _decode(**over):

@@ -75,6 +75,24 @@ def test_chunks(lq, lk):
     _run([lq], [lk], 2, 2, 64, causal=False)
 
 
+@pytest.mark.parametrize("q_lens,k_lens,hq,hkv,d", [
+    ([1], [9000], 4, 1, 128), ([130], [5000], 10, 2, 64), ([40], [3000], 2, 1, 256),
+    ([20, 0, 200, 5], [6000, 4000, 30, 7000], 4, 2, 128), ([3000], [3000], 1, 1, 128),
+    ([300], [20000], 8, 8, 64)])
+def test_few_queries_over_long_keys_are_split(q_lens, k_lens, hq, hkv, d):
+    """Keys split over workgroups (with sequences too short to split among them): the same bits in
+    any workspace, and what lies behind the sequences does not reach them."""
+    need = fq.attn_prefill_workspace_size(len(q_lens), sum(q_lens) + 9, sum(k_lens) + 9, hq, hkv, d)
+    assert need > 0
+    q, k, v, a, b, out, lse = _run(q_lens, k_lens, hq, hkv, d, tail=9)
+    n = sum(q_lens)
+    for fill in (0, 0xFF):
+        ws = torch.full((need,), fill, dtype=torch.uint8, device=DEV)
+        got = fq.attn_prefill(q, k, v, a, hq, hkv, d, cu_seqlens_k=b, workspace=ws)
+        assert torch.equal(got[:n], out[:n])
+    _run(q_lens, k_lens, hq, hkv, d, causal=False, seed=5)
+
+
 @pytest.mark.parametrize("seqs", [64, 65, 256, 257, 700])
 def test_many_sequences(seqs):
     """More sequences than a wave has lanes, and than the ordered search takes."""
