@@ -567,20 +567,26 @@ def fp8_kv_amax(k: torch.Tensor, v: torch.Tensor, amax2: torch.Tensor,
     return amax2
 
 
-def _head_rows(t: torch.Tensor, name: str, heads: int, head_dim: int):
+def _head_rows(t: torch.Tensor, name: str, heads: int, head_dim: int, tokens: int | None = None):
     """(rows, row stride) of a [tokens, heads * head_dim] or [tokens, heads, head_dim] tensor
     whose rows are packed (a column view of a wider buffer is fine)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     e, shape = heads * head_dim, t.shape
-    if not (len(shape) == 2 and shape[1] == e or
-            len(shape) == 3 and shape[1] == heads and shape[2] == head_dim):
+    if len(shape) == 2 and shape[1] == e:
+        n, (stride, inner) = shape[0], t.stride()
+        packed = inner == 1 or e == 1
+    elif len(shape) == 3 and shape[1] == heads and shape[2] == head_dim:
+        n, stride = shape[0], t.stride(0)
+        packed = n == 0 or t[0].is_contiguous()
+    else:
         raise ValueError(f"{name} must be [tokens, {heads} * {head_dim}] or [tokens, {heads}, "
                          f"{head_dim}] (got {tuple(shape)})")
-    n, strides = shape[0], t.stride()
-    if n and not (len(shape) == 2 and strides[1] == 1) and not t[0].is_contiguous():
+    if not packed:
         raise ValueError(f"{name}'s rows must be packed")
-    return n, strides[0] if n > 1 else e
+    if tokens is not None and n != tokens:
+        raise ValueError(f"{name} has {n} rows, q has {tokens}")
+    return n, stride if n > 1 else e
 
 
 def _ptr(t: torch.Tensor, name: str, dtypes, index: int, contiguous: bool = True):
@@ -603,7 +609,7 @@ def _gpu_index(t: torch.Tensor, name: str) -> int:
 def _call(fn: str, index: int, stream, *args) -> None:
     """Calls the library with `index` as the current device, on `stream` (the tensors' device's
     current one when None); raises on an error status."""
-    if torch.cuda.current_device() != index:
+    if torch._C._cuda_getDevice() != index:
         with torch.cuda.device(index):
             return _call(fn, index, stream, *args)
     if stream is None:
@@ -613,7 +619,6 @@ def _call(fn: str, index: int, stream, *args) -> None:
         check(fn, st)
 
 
-_BF16S, _U8S = _BF16, _U8
 _F32S, _I32S, _I64S, _BYTES = (torch.float32,), (torch.int32,), (torch.int64,), (torch.uint8,)
 
 
@@ -627,8 +632,7 @@ def _on_stream(stream, device):
 def _norm_rope(fn, q, k, v, positions, cos_sin, num_q_heads, num_kv_heads, head_dim, q_weight,
                k_weight, eps, interleaved, q_out, k_out, cache, stream):
     t, qs = _head_rows(q, "q", num_q_heads, head_dim)
-    tk, ks = _head_rows(k, "k", num_kv_heads, head_dim)
-    rows = {"k": tk}
+    _, ks = _head_rows(k, "k", num_kv_heads, head_dim, t)
     if q_out is None or k_out is None and cache is None:
         with _on_stream(stream, q.device):
             if q_out is None:
@@ -636,41 +640,38 @@ def _norm_rope(fn, q, k, v, positions, cos_sin, num_q_heads, num_kv_heads, head_
             if k_out is None and cache is None:
                 k_out = torch.zeros((t, num_kv_heads * head_dim), dtype=torch.bfloat16,
                                     device=q.device)
-    rows["q_out"], qos = _head_rows(q_out, "q_out", num_q_heads, head_dim)
+    _, qos = _head_rows(q_out, "q_out", num_q_heads, head_dim, t)
     kos = num_kv_heads * head_dim
     if k_out is not None:
-        rows["k_out"], kos = _head_rows(k_out, "k_out", num_kv_heads, head_dim)
-    if v is not None:
-        rows["v"], vs = _head_rows(v, "v", num_kv_heads, head_dim)
-    if (positions is None) != (cos_sin is None):
-        raise ValueError("pass both positions and cos_sin, or neither")
-    npos, rot = 0, 0
-    if cos_sin is not None:
-        if cos_sin.dim() != 2:
-            raise ValueError("cos_sin must be [num_positions, rot_dim]")
+        _, kos = _head_rows(k_out, "k_out", num_kv_heads, head_dim, t)
+    npos = rot = 0
+    if cos_sin is not None and positions is not None:
         npos, rot = cos_sin.shape
-        rows["positions"] = positions.numel()
+        if positions.numel() != t:
+            raise ValueError(f"positions has {positions.numel()} rows, q has {t}")
+    elif cos_sin is not None or positions is not None:
+        raise ValueError("pass both positions and cos_sin, or neither")
+    if q_weight is not None and q_weight.numel() != head_dim:
+        raise ValueError("q_weight must hold head_dim values")
+    if k_weight is not None and k_weight.numel() != head_dim:
+        raise ValueError("k_weight must hold head_dim values")
     if cache is not None:
-        rows["slot_mapping"] = cache[2].numel()
-    for name, n in rows.items():
-        if n != t:
-            raise ValueError(f"{name} has {n} rows, q has {t}")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None and w.numel() != head_dim:
-            raise ValueError(f"{name} must hold head_dim values")
-    i = _gpu_index(q, "q")
-    args = (_ptr(q_weight, "q_weight", _BF16S, i), _ptr(k_weight, "k_weight", _BF16S, i), eps,
-            _ptr(positions, "positions", _I64S, i), _ptr(cos_sin, "cos_sin", _F32S, i), npos, rot,
-            1 if interleaved else 0)
-    qp, kp = _ptr(q, "q", _BF16S, i, False), _ptr(k, "k", _BF16S, i, False)
-    qop, kop = _ptr(q_out, "q_out", _BF16S, i, False), _ptr(k_out, "k_out", _BF16S, i, False)
-    if cache is None:
-        _call(fn, i, stream, qp, kp, *args, t, num_q_heads, num_kv_heads, head_dim, qs, ks, qop, kop,
-              qos, kos)
-    else:
         k_cache, v_cache, slots, bs, blocks, cs, k_scale, v_scale = cache
-        _call(fn, i, stream, qp, kp, _ptr(v, "v", _BF16S, i, False), *args,
-              _ptr(k_cache, "k_cache", _U8S, i), _ptr(v_cache, "v_cache", _U8S, i),
+        _, vs = _head_rows(v, "v", num_kv_heads, head_dim, t)
+        if slots.numel() != t:
+            raise ValueError(f"slot_mapping has {slots.numel()} rows, q has {t}")
+    i = _gpu_index(q, "q")
+    qp, kp = _ptr(q, "q", _BF16, i, False), _ptr(k, "k", _BF16, i, False)
+    qop, kop = _ptr(q_out, "q_out", _BF16, i, False), _ptr(k_out, "k_out", _BF16, i, False)
+    qwp, kwp = _ptr(q_weight, "q_weight", _BF16, i), _ptr(k_weight, "k_weight", _BF16, i)
+    pp, cp = _ptr(positions, "positions", _I64S, i), _ptr(cos_sin, "cos_sin", _F32S, i)
+    turn = 1 if interleaved else 0
+    if cache is None:
+        _call(fn, i, stream, qp, kp, qwp, kwp, eps, pp, cp, npos, rot, turn, t, num_q_heads,
+              num_kv_heads, head_dim, qs, ks, qop, kop, qos, kos)
+    else:
+        _call(fn, i, stream, qp, kp, _ptr(v, "v", _BF16, i, False), qwp, kwp, eps, pp, cp, npos, rot,
+              turn, _ptr(k_cache, "k_cache", _U8, i), _ptr(v_cache, "v_cache", _U8, i),
               _ptr(slots, "slot_mapping", _I64S, i), t, num_q_heads, num_kv_heads, head_dim, bs,
               blocks, k_scale, v_scale, qs, ks, vs, cs, qop, kop, qos, kos)
     return q_out, k_out
@@ -712,7 +713,7 @@ def fp8_qk_norm_rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
 
 
 def _check_lse(lse, rows, heads):
-    if lse is not None and tuple(lse.shape) != (rows, heads):
+    if lse is not None and lse.shape != (rows, heads):
         raise ValueError(f"lse must be [{rows}, {heads}]")
 
 
@@ -730,18 +731,21 @@ def _attn_workspace(fn: str, index: int, stream, *shape):
     """A workspace for a call of this shape on `stream` of GPU `index`, kept and reused by later
     calls there; None where none is needed.  While a graph is being captured a new one is made
     instead, in the graph's own memory, so that no two graphs share one."""
+    need = _ATTN_SIZES.get((fn, index, shape))
+    if need == 0:
+        return None
     if torch.cuda.current_device() != index:
         with torch.cuda.device(index):
             return _attn_workspace(fn, index, stream, *shape)
-    need = _ATTN_SIZES.get((fn, index, shape))
     if need is None:
-        need = _ATTN_SIZES[(fn, index, shape)] = _workspace_size(fn, *shape)
-    if need == 0:
-        return None
+        if len(_ATTN_SIZES) >= 4096:
+            _ATTN_SIZES.clear()
+        _ATTN_SIZES[(fn, index, shape)] = _workspace_size(fn, *shape)
+        return _attn_workspace(fn, index, stream, *shape)
     if stream is not None and stream != torch._C._cuda_getCurrentRawStream(index):
         with _on_stream(stream, torch.device("cuda", index)):
             return _attn_workspace(fn, index, None, *shape)
-    if torch.cuda.is_current_stream_capturing():
+    if torch._C._cuda_isCurrentStreamCapturing():
         return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
     key = (index, torch._C._cuda_getCurrentRawStream(index))
     ws = _ATTN_WORKSPACES.get(key)
@@ -773,27 +777,28 @@ def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q
     tq, qs = _head_rows(q, "q", num_q_heads, head_dim)
     tk, ks = _head_rows(k, "k", num_kv_heads, head_dim)
     tv, vs = _head_rows(v, "v", num_kv_heads, head_dim)
-    if cu_seqlens_k is None:
-        cu_seqlens_k = cu_seqlens_q
     if tv != tk:
         raise ValueError(f"k has {tk} rows, v has {tv}")
-    if cu_seqlens_q.numel() < 1 or cu_seqlens_k.numel() != cu_seqlens_q.numel():
+    entries = cu_seqlens_q.numel()
+    if cu_seqlens_k is None:
+        cu_seqlens_k = cu_seqlens_q
+    elif cu_seqlens_k.numel() != entries:
+        entries = 0
+    if entries < 1:
         raise ValueError("cu_seqlens_q and cu_seqlens_k must hold num_seqs + 1 entries each")
     if out is None:
         with _on_stream(stream, q.device):
             out = torch.zeros((tq, num_q_heads * head_dim), dtype=torch.bfloat16, device=q.device)
-    to, os_ = _head_rows(out, "out", num_q_heads, head_dim)
-    if to != tq:
-        raise ValueError(f"out has {to} rows, q has {tq}")
+    _, os_ = _head_rows(out, "out", num_q_heads, head_dim, tq)
     _check_lse(lse, tq, num_q_heads)
     i = _gpu_index(q, "q")
-    seqs = cu_seqlens_q.numel() - 1
+    seqs = entries - 1
     if workspace is None:
         workspace = _attn_workspace("attn_prefill_workspace_size", i, stream, seqs, tq, tk,
                                     num_q_heads, num_kv_heads, head_dim)
-    _call("attn_prefill", i, stream, _ptr(q, "q", _BF16S, i, False), _ptr(k, "k", _BF16S, i, False),
-          _ptr(v, "v", _BF16S, i, False), _ptr(cu_seqlens_q, "cu_seqlens_q", _I32S, i),
-          _ptr(cu_seqlens_k, "cu_seqlens_k", _I32S, i), _ptr(out, "out", _BF16S, i, False),
+    _call("attn_prefill", i, stream, _ptr(q, "q", _BF16, i, False), _ptr(k, "k", _BF16, i, False),
+          _ptr(v, "v", _BF16, i, False), _ptr(cu_seqlens_q, "cu_seqlens_q", _I32S, i),
+          _ptr(cu_seqlens_k, "cu_seqlens_k", _I32S, i), _ptr(out, "out", _BF16, i, False),
           _ptr(lse, "lse", _F32S, i), seqs, tq, tk, num_q_heads, num_kv_heads, head_dim,
           head_dim ** -0.5 if softmax_scale is None else softmax_scale, 1 if causal else 0, qs, ks,
           vs, os_, _ptr(workspace, "workspace", _BYTES, i),
@@ -823,17 +828,16 @@ def fp8_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     n, qs = _head_rows(q, "q", num_q_heads, head_dim)
     cs = block_size * num_kv_heads * head_dim if cache_stride is None else cache_stride
     blocks = _kv_num_blocks(k_cache, v_cache, cs)
-    if block_tables.dim() != 2 or block_tables.shape[0] != n or context_lens.numel() != n:
+    if len(block_tables.shape) != 2 or block_tables.shape[0] != n or context_lens.numel() != n:
         raise ValueError("block_tables must be [num_seqs, max_blocks], context_lens [num_seqs]")
     width = block_tables.shape[1]
-    if n and width and not block_tables[0].is_contiguous():
+    table_stride, inner = block_tables.stride()
+    if inner != 1 and width > 1:
         raise ValueError("block_tables' rows must be packed")
     if out is None:
         with _on_stream(stream, q.device):
             out = torch.empty((n, num_q_heads * head_dim), dtype=torch.bfloat16, device=q.device)
-    to, os_ = _head_rows(out, "out", num_q_heads, head_dim)
-    if to != n:
-        raise ValueError(f"out has {to} rows, q has {n}")
+    _, os_ = _head_rows(out, "out", num_q_heads, head_dim, n)
     _check_lse(lse, n, num_q_heads)
     i = _gpu_index(q, "q")
     if n == 0:
@@ -841,11 +845,11 @@ def fp8_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     if workspace is None:
         workspace = _attn_workspace("fp8_attn_decode_workspace_size", i, stream, n, num_q_heads,
                                     num_kv_heads, head_dim)
-    _call("fp8_attn_decode", i, stream, _ptr(q, "q", _BF16S, i, False),
-          _ptr(k_cache, "k_cache", _U8S, i), _ptr(v_cache, "v_cache", _U8S, i),
+    _call("fp8_attn_decode", i, stream, _ptr(q, "q", _BF16, i, False),
+          _ptr(k_cache, "k_cache", _U8, i), _ptr(v_cache, "v_cache", _U8, i),
           _ptr(block_tables, "block_tables", _I32S, i, False),
-          _ptr(context_lens, "context_lens", _I32S, i), _ptr(out, "out", _BF16S, i, False),
-          _ptr(lse, "lse", _F32S, i), n, width, block_tables.stride(0) if n > 1 else width,
+          _ptr(context_lens, "context_lens", _I32S, i), _ptr(out, "out", _BF16, i, False),
+          _ptr(lse, "lse", _F32S, i), n, width, table_stride if n > 1 else width,
           num_q_heads, num_kv_heads, head_dim, block_size, blocks, k_scale, v_scale,
           head_dim ** -0.5 if softmax_scale is None else softmax_scale, qs, os_, cs,
           _ptr(workspace, "workspace", _BYTES, i), workspace.numel())
