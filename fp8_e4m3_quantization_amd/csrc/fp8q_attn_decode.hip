@@ -36,6 +36,7 @@ namespace {
 constexpr int kDecTile = 32;                        // positions a wave takes at a time
 constexpr int kDecRows = 16;                        // query heads of a workgroup
 constexpr int kDecPerCu = 1;                        // workgroups on a CU at once
+constexpr int kWholeMost = 1024;                    // histories up to this long are not cut
 constexpr int kJoinAtOnce = 8;                      // parts whose sums a thread has in flight
 
 struct DecodeArgs {
@@ -51,7 +52,7 @@ struct DecodeArgs {
   int row_tiles;     // ceil(group / 16)
   int heads;         // heads of work: KV heads times row tiles
   int together;      // heads of work of a workgroup: a power of two, at most its waves
-  int shares;        // places for shares of a head
+  int shares;        // places for shares of a head; 0: one share for each sequence
   int rows_most;     // min(group, 16)
   float scale_log2, v_scale;
 };
@@ -168,6 +169,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D == 256 ? 1 : 2) void decode_kerne
   const int sets = a.heads / a.together;
   const int share = blockIdx.x / (8 * sets) * 8 + blockIdx.x % 8;
   const int hw0 = blockIdx.x / 8 % sets * a.together;  // first head of work here
+  if (a.shares == 0 && share >= a.seqs) return;
   const int turn = wave / a.together, turns = kDecWaves / a.together;
   const int hw = hw0 + wave % a.together;          // this wave's
   const int kvh = hw / a.row_tiles;
@@ -175,12 +177,20 @@ __global__ __launch_bounds__(64 * kDecWaves, D == 256 ? 1 : 2) void decode_kerne
   auto head_of = [&](int h) { return h / a.row_tiles * a.group + h % a.row_tiles * kDecRows; };
   const int rows = rows_of(hw);
 
-  int first_steps, first_upto;
-  const Cut cut = cut_up(a, kDecWaves, &first_steps, &first_upto);
-  int step = share * cut.each, seq_start = 0, seq = 0;
-  if (step >= cut.all) return;
-  const int share_end = min(step + cut.each, cut.all);
-  for (int s0 = 0; s0 < a.seqs; s0 += 64) {
+  int first_steps = 0, first_upto = 0;
+  Cut cut;
+  int step = 0, seq_start = 0, seq = 0, share_end = 0;
+  if (a.shares == 0) {  // this sequence, whole
+    cut.step = kDecTile * turns;
+    cut.each = 1 << 30;
+    seq = share;
+  } else {
+    cut = cut_up(a, kDecWaves, &first_steps, &first_upto);
+    step = share * cut.each;
+    if (step >= cut.all) return;
+    share_end = min(step + cut.each, cut.all);
+  }
+  for (int s0 = 0; a.shares > 0 && s0 < a.seqs; s0 += 64) {
     const int n = s0 == 0 ? first_steps : cut.steps_at(a, s0 + lane);
     const int upto = s0 == 0 ? first_upto : wave_prefix(n), here = __builtin_amdgcn_readlane(upto, 63);
     if (step < seq_start + here) {
@@ -199,10 +209,10 @@ __global__ __launch_bounds__(64 * kDecWaves, D == 256 ? 1 : 2) void decode_kerne
 
   while (true) {  // over the share's pieces of sequences
   const SeqPlace sp = cut.seq_at(a, seq, seq_start);
-  const int piece_end = min(sp.end, share_end);
+  const int piece_end = a.shares == 0 ? sp.end : min(sp.end, share_end);
   const int begin = (step - seq_start) * cut.step;
   const int end = min((piece_end - seq_start) * cut.step, sp.len);
-  const int part = share - sp.first_share;
+  const int part = a.shares == 0 ? 0 : share - sp.first_share;
   const int32_t* table = a.tables + seq * a.ts;
 
   // A tile's K and V: lane (g, col) holds K of positions col and 16 + col, and kOut bytes of V
@@ -440,13 +450,22 @@ struct DecodePlan {
   int row_tiles, heads, together, shares, rows;
   uint64_t parts_bytes, bytes;
 };
-DecodePlan decode_plan(int32_t hq, int32_t hkv, int32_t d) {
+// `most`: the longest history that the table has room for.
+DecodePlan decode_plan(int32_t hq, int32_t hkv, int32_t d, int32_t seqs, int64_t most) {
   DecodePlan p = {};
   const int group = hq / hkv;
   p.row_tiles = (group + kDecRows - 1) / kDecRows;
   p.heads = hkv * p.row_tiles;
   p.rows = group < kDecRows ? group : kDecRows;
   p.together = 1;
+  // Short histories: a sequence is a share, with no second kernel, and one head for all the
+  // waves of a workgroup as long as that leaves no CU with two.
+  if (most <= kWholeMost) {
+    while (p.together < waves_of(d) && p.heads % (2 * p.together) == 0 &&
+           int64_t(seqs) * (p.heads / p.together) > num_cus())
+      p.together *= 2;
+    return p;
+  }
   while (p.together < waves_of(d) && p.heads % (2 * p.together) == 0) p.together *= 2;
   const int sets = p.heads / p.together;
   p.shares = kDecPerCu * num_cus() / sets / 8 * 8;
@@ -469,7 +488,8 @@ extern "C" int fp8_attn_decode_workspace_size(int32_t num_seqs, int32_t num_q_he
   *bytes = 0;
   const int rc = decode_shape(num_seqs, num_q_heads, num_kv_heads, head_dim);
   if (rc != FP8Q_OK) return rc;
-  if (num_seqs > 0) *bytes = decode_plan(num_q_heads, num_kv_heads, head_dim).bytes;
+  if (num_seqs > 0)
+    *bytes = decode_plan(num_q_heads, num_kv_heads, head_dim, num_seqs, int64_t(1) << 30).bytes;
   return FP8Q_OK;
 }
 
@@ -505,8 +525,11 @@ extern "C" int fp8_attn_decode(const uint16_t* q, const uint8_t* k_cache, const 
       !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(lse, 4) ||
       !aligned(workspace, 256) || q_stride % 8 || out_stride % 8 || cache_stride % 16)
     return FP8Q_EALIGN;
-  const DecodePlan p = decode_plan(num_q_heads, num_kv_heads, head_dim);
-  if (workspace_bytes < p.bytes) return FP8Q_EINVAL;
+  const DecodePlan p = decode_plan(num_q_heads, num_kv_heads, head_dim, num_seqs, most);
+  uint64_t need = 0;
+  if (fp8_attn_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, &need) != FP8Q_OK ||
+      workspace_bytes < need)
+    return FP8Q_EINVAL;
   DecodeArgs a = {};
   a.q = q, a.kc = k_cache, a.vc = v_cache, a.tables = block_tables, a.lens = context_lens;
   a.out = out, a.lse = lse, a.ts = table_stride, a.qs = q_stride, a.os = out_stride;
@@ -518,15 +541,15 @@ extern "C" int fp8_attn_decode(const uint16_t* q, const uint8_t* k_cache, const 
   a.stats = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.parts_bytes);
   a.scale_log2 = softmax_scale * k_scale * kLog2e;
   a.v_scale = v_scale;
-  const int64_t blocks = int64_t(p.shares) * (p.heads / p.together);
+  const int64_t blocks = (p.shares > 0 ? int64_t(p.shares) : (int64_t(num_seqs) + 7) / 8 * 8) *
+                         (p.heads / p.together);
   const int64_t joins = int64_t(num_seqs) * num_q_heads;
   if (blocks > 0x7FFFFFFF || joins > 0x7FFFFFFF) return FP8Q_EINVAL;
   const int waves = waves_of(head_dim);
   auto kern = head_dim == 64 ? decode_kernel<64> : head_dim == 128 ? decode_kernel<128> : decode_kernel<256>;
   launch(kern, dim3(unsigned(blocks)), dim3(64 * waves), 0, stream, a);
   if (launch_status() != FP8Q_OK) return launch_status();
-  // no history can lie in two shares: nothing to join
-  if (most <= kDecTile) return FP8Q_OK;
+  if (p.shares == 0) return FP8Q_OK;
   // Long rows of parts (few sequences) take many threads, short ones few: 2 sequences of 100 000
   // positions join in 6.8 us with 512 threads a head, 9.3 us with 128; 64 of 4 000 in 11.3 and
   // 5.8 us.

@@ -71,6 +71,13 @@ __device__ __forceinline__ bool find_tile(const PrefillArgs& a, int rows, int ra
     if (s < a.seqs) seq_span(a.cu_q, s, a.tq, &st, &n);
     return (n + rows - 1) / rows;
   };
+  if (a.seqs == 1) {
+    int st, n;
+    seq_span(a.cu_q, 0, a.tq, &st, &n);
+    *seq = 0;
+    *tile = (n + rows - 1) / rows - 1 - rank;
+    return *tile >= 0;
+  }
   if (a.seqs > kOrderedSeqs) {  // in sequence order
     for (int s0 = 0; s0 < a.seqs; s0 += 64) {
       const int n = tiles_of(s0 + lane);
