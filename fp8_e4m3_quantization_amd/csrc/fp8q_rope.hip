@@ -300,14 +300,14 @@ int rope_run(const RopeArgs& a, int interleaved, hipStream_t stream) {
     return launch_status();
   }
   // Few tokens: a lane group for every head of the token, in one pass.  Many: about six heads a
-  // group, so that its cosines and weights serve them all, and eight workgroups a CU that go on
-  // to further tokens.  4593 tokens of 48 128-wide heads: 26.7 us with 128 threads, 29.8 with 256,
+  // group, so that its cosines and weights serve them all, and as many workgroups as a CU holds,
+  // which go on to further tokens.  4593 tokens of 48 128-wide heads: 26.7 us with 128 threads, 29.8 with 256,
   // 38 with 512; 9000 tokens of 24 64-wide heads: 13.8 us with 64 threads, 16.4 with 128.
   const int64_t all = (heads * lanes + 63) / 64 * 64;
   const bool few = a.tokens <= 2 * num_cus();
   int64_t threads = few ? all : (heads * lanes / 6 + 63) / 64 * 64;
   threads = threads < 64 ? 64 : threads > 1024 ? 1024 : threads;
-  const int64_t most = few ? a.tokens : 8 * int64_t(num_cus());
+  const int64_t most = few ? a.tokens : 2048 / threads * num_cus();
   const unsigned blocks = unsigned(a.tokens < most ? a.tokens : most);
   void (*kern)(RopeArgs) = nullptr;
   switch (lanes) {
