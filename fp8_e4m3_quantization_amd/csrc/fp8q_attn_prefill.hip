@@ -191,9 +191,14 @@ typedef __attribute__((address_space(3))) void lds_void;
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 
-// Bits set where one of the two bf16 in w is an infinity or NaN (exponent all ones).
-__device__ __forceinline__ uint32_t non_finite(uint32_t w) {
-  return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+// Two bf16, infinities and NaNs replaced by the largest finite value of their sign: as integers
+// the positive ones lie above 0x7F7F, the negative ones (unsigned) above 0xFF7F.
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  typedef short v2s __attribute__((ext_vector_type(2)));
+  typedef unsigned short v2us __attribute__((ext_vector_type(2)));
+  const v2us below = __builtin_elementwise_min(__builtin_bit_cast(v2us, w), v2us{0xFF7F, 0xFF7F});
+  const v2s x = __builtin_elementwise_min(__builtin_bit_cast(v2s, below), v2s{0x7F7F, 0x7F7F});
+  return __builtin_bit_cast(uint32_t, x);
 }
 
 // The order of a turn of the pipeline below: the score products with the previous tile's weights
@@ -246,11 +251,10 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
   const int kv0 = it.kv0 + from, lk = min(it.lk - from, tiles * kTileKeys);
   auto seen = [&](int i) { return min(max(it.seen(a, i) - from, 0), lk); };
   const int limit = row < lq ? seen(row) : 0;
-  const int wave_limit =
-      __builtin_amdgcn_readfirstlane(mine < lq ? seen(min(mine + kWaveRows, lq) - 1) : 0);
-  // tiles that every query of the workgroup sees whole: an odd number, or none
-  const int sees_all = __builtin_amdgcn_readfirstlane(seen(first) / kTileKeys);
-  const int whole = sees_all - (sees_all > 0 && sees_all % 2 == 0);
+  // this wave's tiles: those that some of its queries see; those that all of them see whole
+  const int my_tiles = __builtin_amdgcn_readfirstlane(
+      mine < lq ? (seen(min(mine + kWaveRows, lq) - 1) + kTileKeys - 1) / kTileKeys : 0);
+  const int my_whole = __builtin_amdgcn_readfirstlane(mine < lq ? seen(mine) / kTileKeys : 0);
 
   v8bf qf[D / 16];
   {
@@ -313,6 +317,8 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
   for (int i = 0; i < D / 32; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
+  uint32_t odd = 0;       // not 0: values of the last tiles were held to finite ones
+  int first_held = 0;     // the first of those tiles
   const float scale = a.scale_log2;
   float ref = neg_inf(), sum = 0.0f;  // reference (log2 units) and this half's weights
 
@@ -365,122 +371,124 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
     }
     return __builtin_bit_cast(v8bf, v4u{w[0], w[1], w[2], w[3]});
   };
-  // O^T += V^T P^T over 16 keys.
-  auto add_values = [&](const uint16_t* vt, int st, v8bf p) {
+  // V^T of 16 keys (step st of the tile) and 32 values, in the order of the weights.
+  auto v_frag = [&](const uint16_t* vt, int st, int i) {
     const int i16 = lane & 15, side = (lane >> 4) & 1;
+    const int ra = 16 * st + 4 * half + (i16 >> 2), c = 4 * i + 2 * side + ((i16 & 3) >> 1);
+    const int within = 4 * (i16 & 1);
+    const v2u lo = __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_v4s*)(vt + ra * D + v_chunk<D>(ra, c) * 8 + within)));
+    const v2u hi = __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_v4s*)(vt + (ra + 8) * D + v_chunk<D>(ra + 8, c) * 8 + within)));
+    return v4u{lo[0], lo[1], hi[0], hi[1]};
+  };
+  // O^T += V^T P^T over 16 keys.  With kEdge, infinities and NaNs are held to the largest finite
+  // values, so that a weight of 0 gives 0; returns a word that is not 0 where there were any.
+  auto add_values = [&](const uint16_t* vt, int st, v8bf p, auto edge) {
+    constexpr bool kEdge = decltype(edge)::value;
+    uint32_t odd = 0;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-      const int ra = 16 * st + 4 * half + (i16 >> 2), c = 4 * i + 2 * side + ((i16 & 3) >> 1);
-      const int within = 4 * (i16 & 1);
-      const v2u lo = __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (lds_v4s*)(vt + ra * D + v_chunk<D>(ra, c) * 8 + within)));
-      const v2u hi = __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (lds_v4s*)(vt + (ra + 8) * D + v_chunk<D>(ra + 8, c) * 8 + within)));
-      o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, v4u{lo[0], lo[1], hi[0], hi[1]}),
-                                                     p, o[i], 0, 0, 0);
-    }
-  };
-  // A tile that some query does not see whole may hold infinities or NaNs where it does not look,
-  // and a weight of 0 times those is not 0.  They are rare: a tile that has any has them added,
-  // key by key, to the queries that see them, and zeroed in LDS before the products.
-  auto odd_in = [&](const uint16_t* vt) {
-    uint32_t any = 0;
+      v4u w = v_frag(vt, st, i);
+      if (kEdge) {
 #pragma unroll
-    for (int j = 0; j < kCopies; ++j) {
-      const uint4 x = *reinterpret_cast<const uint4*>(vt + ((wave + kWaves * j) * 64 + lane) * 8);
-      any |= non_finite(x.x) | non_finite(x.y) | non_finite(x.z) | non_finite(x.w);
-    }
-    return __syncthreads_or(any != 0) != 0;
-  };
-  auto take_odd = [&](int t, uint16_t* vt) {
-    for (int j = 0; j < kTileKeys; ++j)
-      if (t * kTileKeys + j < limit) {
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int e = 32 * i + 8 * (r >> 2) + 4 * half + (r & 3);
-            const uint32_t x = vt[j * D + v_chunk<D>(j, e >> 3) * 8 + (e & 7)];
-            if (non_finite(x)) o[i][r] += __uint_as_float(x << 16);
-          }
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t x = finite2(w[e]);
+          odd |= x ^ w[e];
+          w[e] = x;
+        }
+        asm volatile("" : "+v"(odd));  // taken up here: the values as read need not be kept
       }
-    __syncthreads();
-    for (int j = threadIdx.x; j < kTileKeys * D; j += 64 * kWaves)
-      if (non_finite(vt[j])) vt[j] = 0;
-    __syncthreads();
+      o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, w), p, o[i], 0, 0, 0);
+    }
+    return odd;
   };
   auto landed = [&]() {
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's copies landed
     __syncthreads();                     // every wave's have, and the other buffers are free
   };
-  // One turn of the pipeline: the scores of tile t + 1 (matrix cores) beside the weights of tile t
-  // (vector ALUs), then tile t's values (matrix cores) beside the largest of the new scores.
-  auto turn = [&](int t, const v16f* s, v16f* next, const uint16_t* kn, const uint16_t* vt,
-                  uint16_t* k_free, uint16_t* v_free) {
+  // Every wave passes one barrier a tile, and at it starts the copies of the next tile's values and
+  // of the keys after those.
+  auto next_tile = [&](uint16_t* k_free, uint16_t* v_free) {
     landed();
     copy_next(ksrc, k_free);
     copy_next(vsrc, v_free);
+  };
+  // One turn of the pipeline, for tiles that the wave sees whole: the scores of tile t + 1 (matrix
+  // cores) beside the weights of tile t (vector ALUs), then tile t's values (matrix cores) beside
+  // the largest of the new scores.
+  auto turn = [&](const v16f* s, v16f* next, const uint16_t* kn, const uint16_t* vt,
+                  uint16_t* k_free, uint16_t* v_free) {
+    next_tile(k_free, v_free);
     const float base = ref == neg_inf() ? 0.0f : ref;
     products(next, kn);
     v8bf p[4];
 #pragma unroll
     for (int st = 0; st < 4; ++st) p[st] = weights(s, st, base);
 #pragma unroll
-    for (int st = 0; st < 4; ++st) add_values(vt, st, p[st]);
+    for (int st = 0; st < 4; ++st) add_values(vt, st, p[st], std::false_type{});
     const float top = largest(next);
-    pair_up<D>();
+    if constexpr (D == 128) pair_up<D>();
     move_to(top);
   };
-  v16f sa[2];
-  int t = 0;
-  if (whole > 0) {
-    v16f sb[2];
+  auto mask = [&](int t, v16f* s) {
+    const int left = limit - t * kTileKeys - 4 * half;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        s[b][r] = 32 * b + 8 * (r >> 2) + (r & 3) < left ? s[b][r] : neg_inf();
+        if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // few conditions alive at a time
+      }
+  };
+  if (tiles > 0) {
+    v16f sa[2];
     copy_next(ksrc, k0);
     landed();
     copy_next(ksrc, k1);
     copy_next(vsrc, v0);
-    products(sa, k0);
-    move_to(largest(sa));
-    for (; t + 1 < whole; t += 2) {
-      turn(t, sa, sb, k1, v0, k0, v1);
-      turn(t + 1, sb, sa, k0, v1, k1, v0);
-    }
-    landed();
-    copy_next(vsrc, v1);
-    const float base = ref == neg_inf() ? 0.0f : ref;
-#pragma unroll
-    for (int st = 0; st < 4; ++st) add_values(v0, st, weights(sa, st, base));
-    ++t;
-  } else if (tiles > 0) {
-    copy_next(ksrc, k0);
-    copy_next(vsrc, v0);
-  }
-  for (; t < tiles; ++t) {
-    uint16_t *kt = t & 1 ? k1 : k0, *vt = t & 1 ? v1 : v0;
-    landed();
-    copy_next(ksrc, t & 1 ? k0 : k1);
-    copy_next(vsrc, t & 1 ? v0 : v1);
-    const bool odd = odd_in(vt), mine_too = t * kTileKeys < wave_limit;
-    if (mine_too) {
-      const int left = limit - t * kTileKeys - 4 * half;
-      products(sa, kt);
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          sa[b][r] = 32 * b + 8 * (r >> 2) + (r & 3) < left ? sa[b][r] : neg_inf();
-          if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // few conditions alive at a time
-        }
+    if (my_tiles > 0) {
+      products(sa, k0);
+      if (my_whole == 0) mask(0, sa);
       move_to(largest(sa));
     }
-    if (odd) take_odd(t, vt);
-    if (mine_too) {
+    int t = 0;
+    for (; t + 2 < my_whole; t += 2) {
+      v16f sb[2];
+      turn(sa, sb, k1, v0, k0, v1);
+      turn(sb, sa, k0, v1, k1, v0);
+    }
+    first_held = t;
+    for (; t < my_tiles; ++t) {  // the last tiles, among them those that are seen in part
+      uint16_t *kt = t & 1 ? k1 : k0, *vt = t & 1 ? v1 : v0;
+      next_tile(kt, t & 1 ? v0 : v1);
       const float base = ref == neg_inf() ? 0.0f : ref;
 #pragma unroll
-      for (int st = 0; st < 4; ++st) add_values(vt, st, weights(sa, st, base));
+      for (int st = 0; st < 4; ++st) odd |= add_values(vt, st, weights(sa, st, base), std::true_type{});
+      if (t + 1 < my_tiles) {
+        products(sa, t & 1 ? k0 : k1);
+        if (t + 1 >= my_whole) mask(t + 1, sa);
+        move_to(largest(sa));
+      }
     }
+    for (; t < tiles; ++t) next_tile(t & 1 ? k1 : k0, t & 1 ? v0 : v1);
   }
 
+  // Infinities and NaNs that were held to finite values reach the queries that see them (rare).
+  if (__any(odd != 0)) {
+    for (int j = first_held * kTileKeys; j < limit; ++j) {
+      const uint16_t* src = a.v + int64_t(kv0 + j) * a.vs + int64_t(kvh) * D + 4 * half;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+          const uint2 x = *reinterpret_cast<const uint2*>(src + 32 * i + 2 * r);
+          const float f[4] = {bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y)};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][r + e] += __builtin_isfinite(f[e]) ? 0.0f : f[e];
+        }
+    }
+  }
   const float total = sum_over_halves(sum);
   if (row >= lq) return;
   if (parts > 1) {
@@ -509,7 +517,7 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
 }
 
 template <int D>
-__global__ __launch_bounds__(64 * kPrefillWaves, D == 256 ? 1 : 2) void prefill_kernel(const PrefillArgs a) {
+__global__ __launch_bounds__(64 * kPrefillWaves, D == 256 ? 1 : D == 128 ? 2 : 3) void prefill_kernel(const PrefillArgs a) {
   prefill_tile<D>(a);
 }
 
