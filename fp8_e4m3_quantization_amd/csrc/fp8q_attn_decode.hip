@@ -116,9 +116,9 @@ struct Cut {
   __device__ __forceinline__ int steps_at(const DecodeArgs& a, int s) const {
     return s < a.seqs ? steps_of(seq_len(a, s)) : 0;
   }
-  __device__ __forceinline__ SeqPlace seq_at(const DecodeArgs& a, int s, int start) const {
+  __device__ __forceinline__ SeqPlace seq_at(int len, int start) const {
     SeqPlace p;
-    p.len = __builtin_amdgcn_readfirstlane(seq_len(a, s));
+    p.len = len;
     p.start = start;
     p.end = start + steps_of(p.len);
     p.first_share = start / each;
@@ -126,14 +126,21 @@ struct Cut {
     return p;
   }
 };
-// `first`: lane l's steps of sequence l, and their prefix sums, for the searches that follow.
-__device__ __forceinline__ Cut cut_up(const DecodeArgs& a, int waves, int* first, int* first_upto) {
+// What a lane keeps of sequence `lane` (of the first 64) for the searches that follow.
+struct FirstSeqs {
+  int len, steps, upto;  // length, steps, steps up to and with it
+};
+__device__ __forceinline__ int len_of(const DecodeArgs& a, const FirstSeqs& f, int s) {
+  return s < 64 ? __builtin_amdgcn_readlane(f.len, s) : __builtin_amdgcn_readfirstlane(seq_len(a, s));
+}
+__device__ __forceinline__ Cut cut_up(const DecodeArgs& a, int waves, FirstSeqs* f) {
   Cut c;
   const int lane = threadIdx.x & 63;
   c.step = kDecTile * (waves / a.together);
-  *first = c.steps_at(a, lane);
-  *first_upto = wave_prefix(*first);
-  c.all = __builtin_amdgcn_readlane(*first_upto, 63);
+  f->len = lane < a.seqs ? seq_len(a, lane) : 0;
+  f->steps = lane < a.seqs ? c.steps_of(f->len) : 0;
+  f->upto = wave_prefix(f->steps);
+  c.all = __builtin_amdgcn_readlane(f->upto, 63);
   for (int s0 = 64; s0 < a.seqs; s0 += 64)
     c.all += __builtin_amdgcn_readlane(wave_prefix(c.steps_at(a, s0 + lane)), 63);
   c.each = max((c.all + a.shares - 1) / a.shares, 1);
@@ -177,22 +184,23 @@ __global__ __launch_bounds__(64 * kDecWaves, D == 256 ? 1 : 2) void decode_kerne
   auto head_of = [&](int h) { return h / a.row_tiles * a.group + h % a.row_tiles * kDecRows; };
   const int rows = rows_of(hw);
 
-  int first_steps = 0, first_upto = 0;
+  FirstSeqs firsts = {};
   Cut cut;
   int step = 0, seq_start = 0, seq = 0, share_end = 0;
   if (a.shares == 0) {  // this sequence, whole
     cut.step = kDecTile * turns;
     cut.each = 1 << 30;
     seq = share;
+    firsts.len = seq_len(a, min(lane, a.seqs - 1));
   } else {
-    cut = cut_up(a, kDecWaves, &first_steps, &first_upto);
+    cut = cut_up(a, kDecWaves, &firsts);
     step = share * cut.each;
     if (step >= cut.all) return;
     share_end = min(step + cut.each, cut.all);
   }
   for (int s0 = 0; a.shares > 0 && s0 < a.seqs; s0 += 64) {
-    const int n = s0 == 0 ? first_steps : cut.steps_at(a, s0 + lane);
-    const int upto = s0 == 0 ? first_upto : wave_prefix(n), here = __builtin_amdgcn_readlane(upto, 63);
+    const int n = s0 == 0 ? firsts.steps : cut.steps_at(a, s0 + lane);
+    const int upto = s0 == 0 ? firsts.upto : wave_prefix(n), here = __builtin_amdgcn_readlane(upto, 63);
     if (step < seq_start + here) {
       const int j = __builtin_ctzll(__ballot(upto > step - seq_start));
       seq = s0 + j;
@@ -208,7 +216,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D == 256 ? 1 : 2) void decode_kerne
   const int64_t e = int64_t(a.hkv) * D;
 
   while (true) {  // over the share's pieces of sequences
-  const SeqPlace sp = cut.seq_at(a, seq, seq_start);
+  const SeqPlace sp = cut.seq_at(len_of(a, firsts, seq), seq_start);
   const int piece_end = a.shares == 0 ? sp.end : min(sp.end, share_end);
   const int begin = (step - seq_start) * cut.step;
   const int end = min((piece_end - seq_start) * cut.step, sp.len);
@@ -396,16 +404,16 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const DecodeArgs a, 
   constexpr int kLanes = D / 4, kSlots = kJoinThreads / kLanes;
   const int lane = threadIdx.x & 63;
   const int head = blockIdx.x % a.hq, seq = blockIdx.x / a.hq;
-  int first_steps, first_upto;
-  const Cut cut = cut_up(a, waves, &first_steps, &first_upto);
+  FirstSeqs firsts;
+  const Cut cut = cut_up(a, waves, &firsts);
   int start = 0;
   for (int s0 = 0; s0 <= seq; s0 += 64) {
-    const int n = s0 == 0 ? first_steps : cut.steps_at(a, s0 + lane);
-    const int upto = s0 == 0 ? first_upto : wave_prefix(n);
+    const int n = s0 == 0 ? firsts.steps : cut.steps_at(a, s0 + lane);
+    const int upto = s0 == 0 ? firsts.upto : wave_prefix(n);
     const int j = min(seq - s0, 63);
     start += __builtin_amdgcn_readlane(upto, j) - (seq - s0 < 64 ? __builtin_amdgcn_readlane(n, j) : 0);
   }
-  const SeqPlace sp = cut.seq_at(a, seq, start);
+  const SeqPlace sp = cut.seq_at(len_of(a, firsts, seq), start);
   if (sp.parts == 1) return;
   const int kvh = head / a.group, of_group = head - kvh * a.group;
   const int hw = kvh * a.row_tiles + of_group / kDecRows, r = of_group % kDecRows;
