@@ -48,7 +48,7 @@ struct PrefillArgs {
 };
 
 // Parts that `tiles` tiles of keys are split into: no part is short.
-constexpr int kPartTiles = 8;
+constexpr int kPartTiles = 4;
 __device__ __forceinline__ int parts_of(const PrefillArgs& a, int tiles) {
   return max(min(a.most_parts, tiles / kPartTiles), 1);
 }
@@ -521,23 +521,22 @@ __global__ __launch_bounds__(64 * kPrefillWaves, D == 256 ? 1 : D == 128 ? 2 : 3
   prefill_tile<D>(a);
 }
 
-// Adds up the parts of a work item's queries in order: a D/4-lane group per query at a time.
+// Adds up the parts of a work item's queries in order: D/4 lanes to a query.
 constexpr int kPrefillJoinThreads = 256;
+constexpr int join_rows(int d) { return kPrefillJoinThreads / (d / 4); }
 template <int D>
 __global__ __launch_bounds__(kPrefillJoinThreads) void prefill_join_kernel(const PrefillArgs a) {
-  constexpr int kLanes = D / 4, kGroups = kPrefillJoinThreads / kLanes, kSplits = kPrefillRows / 32;
+  constexpr int kLanes = D / 4, kSplits = kPrefillRows / join_rows(D);
   const int index = blockIdx.x / kSplits;
+  const int r = blockIdx.x % kSplits * join_rows(D) + int(threadIdx.x) / kLanes;
+  const int d = threadIdx.x % kLanes * 4;
   Item it;
   if (!find_item(a, index, &it)) return;
-  const int parts = parts_of(a, it.key_tiles(a));
-  if (parts == 1) return;
-  const int first = blockIdx.x % kSplits * 32, d = threadIdx.x % kLanes * 4;
-  for (int r = first + int(threadIdx.x) / kLanes; r < first + 32; r += kGroups) {
-    const int row = it.tile * kPrefillRows + r;
-    if (row >= it.lq) return;
+  const int parts = parts_of(a, it.key_tiles(a)), row = it.tile * kPrefillRows + r;
+  if (parts > 1 && row < it.lq) {
     float ref = neg_inf(), total = 0.0f;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+#pragma unroll 8
     for (int p = 0; p < parts; ++p) {
       const int64_t at = (int64_t(index) * a.most_parts + p) * kPrefillRows + r;
       const float4 x = *reinterpret_cast<const float4*>(a.sums + at * D + d);
@@ -560,8 +559,10 @@ __global__ __launch_bounds__(kPrefillJoinThreads) void prefill_join_kernel(const
 }
 
 // Work items of a call (an upper bound: tiles of whole sequences), and the parts that their keys
-// are split into: where the items leave half of the device idle and the keys are long, as many
-// as fill it.
+// are split into: the number with the least estimated time.  A workgroup alone on its CU takes
+// about 1 us a tile of 64 keys (128-wide heads), two on one CU about 2; joining parts costs a
+// launch and the way of their sums through memory.  512 queries of 40 heads over 8704 keys: 144 us
+// in one part, 111 in three; 23 queries over 2794 keys, 10 heads: 44 us in one, 17 in eleven.
 struct PrefillPlan {
   int64_t items;
   int parts;
@@ -569,16 +570,30 @@ struct PrefillPlan {
 };
 PrefillPlan prefill_plan(int32_t seqs, int32_t total_q, int32_t total_k, int32_t hq, int32_t d) {
   PrefillPlan p = {};
-  p.items = (int64_t(total_q) / kPrefillRows + seqs) * hq;
-  const int64_t slots = (d == 256 ? 1 : 2) * int64_t(num_cus());
-  const int64_t by_items = slots / p.items;
-  const int64_t by_keys = int64_t(total_k) / seqs / (kTileKeys * kPartTiles);
-  p.parts = int(by_items < by_keys ? by_items : by_keys);
-  if (p.parts < 2) {
-    p.parts = 1;
-    return p;
+  p.items = (int64_t(total_q) + int64_t(seqs) * (kPrefillRows - 1)) / kPrefillRows * hq;
+  p.parts = 1;
+  const int64_t cus = num_cus();
+  const double tile_us = d == 256 ? 2.0 : d == 128 ? 1.0 : 0.7;
+  const double mean = double(total_k) / seqs / kTileKeys;  // tiles of a sequence
+  const double all = double(total_k) / kTileKeys;
+  const double longest = seqs == 1 ? mean : (2 * mean < all ? 2 * mean : all);
+  // under a causal mask prompts without a history see half of their keys in the mean
+  const bool history = total_k > 2 * int64_t(total_q);
+  const double spread = double(p.items) * mean * (history ? 1.0 : 0.5) / cus * tile_us;
+  double best = 0.0;
+  for (int n = 1; n <= 64 && n * kPartTiles <= longest + 1; ++n) {
+    const int64_t groups = p.items * n;
+    if (n > 1 && !history && groups > cus) break;
+    const int64_t rounds = groups <= cus ? 1 : 2 * ((groups + 2 * cus - 1) / (2 * cus));
+    const double path = longest / n * tile_us * rounds;
+    double us = path > spread ? path : spread;
+    if (n > 1) us += 4.0 + double(total_q) * hq * n * d * 8 / 5e6;
+    if (n == 1 || us < best * (p.parts == 1 ? 0.8 : 1.0)) {
+      best = us;
+      p.parts = n;
+    }
   }
-  if (p.parts > 64) p.parts = 64;
+  if (p.parts == 1) return p;
   const uint64_t rows = uint64_t(p.items) * p.parts * kPrefillRows;
   p.sums_bytes = rows * d * 4;
   p.bytes = p.sums_bytes + rows * 8;
@@ -648,7 +663,7 @@ extern "C" int attn_prefill(const uint16_t* q, const uint16_t* k, const uint16_t
   a.stats = p.bytes ? reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.sums_bytes) : nullptr;
   // parts of an item lie 8 workgroups apart: whole eights of items
   const int64_t blocks = p.parts == 1 ? p.items : (p.items + 7) / 8 * 8 * p.parts;
-  const int64_t joins = p.items * (kPrefillRows / 32);
+  const int64_t joins = p.items * (kPrefillRows / join_rows(head_dim));
   if (p.items > 0x7FFFFFFF || blocks > 0x7FFFFFFF || joins > 0x7FFFFFFF) return FP8Q_EINVAL;
   auto kern = head_dim == 64 ? prefill_kernel<64> : head_dim == 128 ? prefill_kernel<128> : prefill_kernel<256>;
   launch(kern, dim3(unsigned(blocks)), dim3(64 * kPrefillWaves), 0, stream, a);
