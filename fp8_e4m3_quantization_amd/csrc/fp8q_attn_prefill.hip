@@ -444,9 +444,9 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
   if (tiles > 0) {
     v16f sa[2];
     copy_next(ksrc, k0);
-    landed();
-    copy_next(ksrc, k1);
     copy_next(vsrc, v0);
+    copy_next(ksrc, k1);
+    landed();
     if (my_tiles > 0) {
       products(sa, k0);
       if (my_whole == 0) mask(0, sa);
