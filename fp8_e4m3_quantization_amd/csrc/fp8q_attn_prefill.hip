@@ -31,6 +31,7 @@ constexpr int kTileKeys = 64;
 constexpr int kWaveRows = 32;
 constexpr int kPrefillWaves = 4;
 constexpr int kPrefillRows = kWaveRows * kPrefillWaves;  // queries of a workgroup
+constexpr float kFar = 0x1p27f;    // a reference whose rounding (2^3) still leaves weights their range
 constexpr int kOrderedSeqs = 256;  // batches up to this size run their longest tiles first
 
 struct PrefillArgs {
@@ -321,6 +322,7 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
   int first_held = 0;     // the first of those tiles
   const float scale = a.scale_log2;
   float ref = neg_inf(), sum = 0.0f;  // reference (log2 units) and this half's weights
+  int far = 0;                        // the current scores stand scaled, less the reference
 
   // S^T of a tile.
   auto products = [&](v16f* s, const uint16_t* kt) {
@@ -346,7 +348,11 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
       for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
     return max_over_halves(top) * scale;
   };
-  auto move_to = [&](float top) {
+  // The reference for the scores s, whose largest (log2 units) is top.  s * scale - ref is one fused
+  // product, exact but for its last rounding, while ref is rounded: by up to 2^-24 of itself, which
+  // every weight of a query shares.  Beyond kFar that could leave binary32's range of exponents;
+  // there the products are rounded too, so that the largest weight is 1 again.
+  auto move_to = [&](float top, v16f* s) {
     const bool moves = top > ref + kSoftmaxSlack;
     if (__any(moves)) {
       const float f = moves ? __builtin_amdgcn_exp2f(ref - top) : 1.0f;
@@ -357,15 +363,24 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[i][r] *= f;
     }
+    const float base = ref == neg_inf() ? 0.0f : ref;
+    far = __any(__builtin_fabsf(base) > kFar);
+    if (far) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[b][r] = s[b][r] * scale - base;
+    }
   };
   // Weights of 16 keys (step st of the tile) as the second product's operand.
-  auto weights = [&](const v16f* s, int st, float base) {
+  auto weights = [&](const v16f* s, int st) {
+    const float mul = far ? 1.0f : scale, base = far || ref == neg_inf() ? 0.0f : ref;
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
       const int r = 8 * (st & 1) + e;
-      const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[st >> 1][r], scale, -base));
-      const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[st >> 1][r + 1], scale, -base));
+      const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[st >> 1][r], mul, -base));
+      const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[st >> 1][r + 1], mul, -base));
       sum += x + y;
       w[e / 2] = cvt_bf16x2(x, y);
     }
@@ -420,16 +435,15 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
   auto turn = [&](const v16f* s, v16f* next, const uint16_t* kn, const uint16_t* vt,
                   uint16_t* k_free, uint16_t* v_free) {
     next_tile(k_free, v_free);
-    const float base = ref == neg_inf() ? 0.0f : ref;
     products(next, kn);
     v8bf p[4];
 #pragma unroll
-    for (int st = 0; st < 4; ++st) p[st] = weights(s, st, base);
+    for (int st = 0; st < 4; ++st) p[st] = weights(s, st);
 #pragma unroll
     for (int st = 0; st < 4; ++st) add_values(vt, st, p[st], std::false_type{});
     const float top = largest(next);
     if constexpr (D == 128) pair_up<D>();
-    move_to(top);
+    move_to(top, next);
   };
   auto mask = [&](int t, v16f* s) {
     const int left = limit - t * kTileKeys - 4 * half;
@@ -450,7 +464,7 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
     if (my_tiles > 0) {
       products(sa, k0);
       if (my_whole == 0) mask(0, sa);
-      move_to(largest(sa));
+      move_to(largest(sa), sa);
     }
     int t = 0;
     for (; t + 2 < my_whole; t += 2) {
@@ -462,13 +476,12 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
     for (; t < my_tiles; ++t) {  // the last tiles, among them those that are seen in part
       uint16_t *kt = t & 1 ? k1 : k0, *vt = t & 1 ? v1 : v0;
       next_tile(kt, t & 1 ? v0 : v1);
-      const float base = ref == neg_inf() ? 0.0f : ref;
 #pragma unroll
-      for (int st = 0; st < 4; ++st) odd |= add_values(vt, st, weights(sa, st, base), std::true_type{});
+      for (int st = 0; st < 4; ++st) odd |= add_values(vt, st, weights(sa, st), std::true_type{});
       if (t + 1 < my_tiles) {
         products(sa, t & 1 ? k0 : k1);
         if (t + 1 >= my_whole) mask(t + 1, sa);
-        move_to(largest(sa));
+        move_to(largest(sa), sa);
       }
     }
     for (; t < tiles; ++t) next_tile(t & 1 ? k1 : k0, t & 1 ? v0 : v1);

@@ -155,6 +155,35 @@ def test_scales(scale):
     _check(s, _call(s, lse=lse, softmax_scale=scale), lse, scale)
 
 
+@pytest.mark.parametrize("unit", [2.0 ** 10, 2.0 ** 40, 2.0 ** 64])  # k_scale's largest
+@pytest.mark.parametrize("lens", [[3000, 70], [300, 1]])
+def test_huge_scores_pick_the_largest(lens, unit):
+    """Scores that are exact multiples of `unit` in binary32: out is the mean of V over the ties.
+    Tolerances as in the prompts' test of this name; here the products are rounded before the
+    reference is taken off, so that the tied weights are 1 and their rounding to bf16 is exact."""
+    s = _setup(lens, 4, 2, 64, 16)
+    codes = torch.randint(-2, 3, s["kc"].shape, device=DEV).float().to(torch.float8_e4m3fn)
+    s["kc"] = codes.view(torch.uint8)
+    s["q"] = torch.randint(-2, 3, s["q"].shape, device=DEV).to(BF16)
+    lse = torch.zeros((2, 4), device=DEV)
+    out = fq.fp8_attn_decode(s["q"], s["kc"], s["vc"], s["tables"], s["lens"], 4, 2, 64, 16, unit, 0.5,
+                             softmax_scale=1.0, lse=lse)
+    kp, vp = (attn_ref.e4m3_values(s[x]).view(-1, 16, 2, 64) for x in ("kc", "vc"))
+    for i, n in enumerate(lens):
+        pos = torch.arange(n, device=DEV)
+        ids = s["tables"][i].long()[pos // 16]
+        for h in range(4):
+            k, v = kp[ids, pos % 16, h // 2], 0.5 * vp[ids, pos % 16, h // 2]
+            score = unit * (k @ s["q"][i].double()[h * 64:(h + 1) * 64])
+            best = (score == score.max()).double()
+            w = best / best.sum()
+            want = w @ v
+            bound = attn_ref.HALF_BF16 * want.abs() + (n + 8) * attn_ref.U24 * (w @ v.abs())
+            attn_ref.check(out[i, h * 64:(h + 1) * 64], want, bound, "out")
+            want = score.max() + torch.log(best.sum())
+            attn_ref.check(lse[i, h], want, 5 * attn_ref.U24 * want.abs() + 2.0 ** -20, "lse")
+
+
 def test_cache_past_four_gib():
     """Blocks whose byte offsets pass 2^32."""
     bs, hkv, d = 16, 4, 128

@@ -126,6 +126,48 @@ def test_large_scores_move_the_reference():
     attn_ref.prefill(q, k, v, [0, n], [0, n], 1, 1, d, d ** -0.5, True, out, lse)
 
 
+@pytest.mark.parametrize("unit", [2.0 ** 10, 2.0 ** 22, 2.0 ** 40, 2.0 ** 80])
+@pytest.mark.parametrize("d,lq,lk,causal", [(64, 200, 200, True), (128, 200, 200, True),
+                                            (256, 200, 200, True), (128, 20, 3000, False)])
+def test_huge_scores_pick_the_largest(d, lq, lk, causal, unit):
+    """Scores that are exact multiples of `unit` in binary32: the weights are 1 at the largest
+    and 0 elsewhere, so out is the mean of v over the ties.  Tolerance: a mean of at most lk terms
+    in binary32 and one rounding to bf16; and, as in attn_ref, half a bf16 step of sum w|v|: the
+    tied weights are 2^e with the reference's rounding e in the exponent, not 1, and are rounded to
+    bf16 in the numerator alone, by a factor within 1 +- 2^-8.  lse: five roundings (scale to log2
+    units, its product, the reference's sum with the log, the constant and product back)."""
+    g = torch.Generator(device=DEV).manual_seed(d + lk)
+    q = (torch.randint(-2, 3, (lq, 2 * d), generator=g, device=DEV) * unit ** 0.5).to(BF16)
+    k = (torch.randint(-2, 3, (lk, d), generator=g, device=DEV) * unit ** 0.5).to(BF16)
+    v = torch.randn((lk, d), generator=g, device=DEV).to(BF16)
+    a = torch.tensor([0, lq], dtype=torch.int32, device=DEV)
+    b = torch.tensor([0, lk], dtype=torch.int32, device=DEV)
+    lse = torch.empty((lq, 2), device=DEV)
+    out = fq.attn_prefill(q, k, v, a, 2, 1, d, cu_seqlens_k=b, softmax_scale=1.0, causal=causal, lse=lse)
+    for h in range(2):
+        s = q[:, h * d:(h + 1) * d].double() @ k.double().t()
+        if causal:
+            s = torch.where(attn_ref.causal_mask(lq, lk, DEV), s, -math.inf)
+        best = (s == s.amax(1, keepdim=True)).double()
+        w = best / best.sum(1, keepdim=True)
+        want, size = w @ v.double(), w @ v.double().abs()
+        bound = attn_ref.HALF_BF16 * (want.abs() + size) + (lk + 8) * attn_ref.U24 * size
+        attn_ref.check(out[:, h * d:(h + 1) * d], want, bound, "out")
+        want = s.amax(1) + torch.log(best.sum(1))
+        attn_ref.check(lse[:, h], want, 5 * attn_ref.U24 * want.abs() + 2.0 ** -20, "lse")
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_smallest_scale(causal):
+    """The smallest scale that a binary32 holds: every seen key counts the same."""
+    n, d = 100, 128
+    q, k, v = (torch.randn((n, d), device=DEV).to(BF16) for _ in range(3))
+    cu = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    lse = torch.empty((n, 1), device=DEV)
+    out = fq.attn_prefill(q, k, v, cu, 1, 1, d, softmax_scale=2.0 ** -149, causal=causal, lse=lse)
+    attn_ref.prefill(q, k, v, [0, n], [0, n], 1, 1, d, 2.0 ** -149, causal, out, lse)
+
+
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
 def test_masked_infinities_and_nans_stay_where_they_are(bad, d):
