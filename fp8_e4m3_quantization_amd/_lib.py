@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import threading
 
 import torch
 
@@ -718,7 +719,17 @@ def _check_lse(lse, rows, heads):
 
 
 _ATTN_SIZES = {}       # (entry point, device index, shape) -> its workspace size there
-_ATTN_WORKSPACES = {}  # (device index, stream) -> uint8 tensor
+
+
+class _Workspaces(threading.local):
+    """(device index, stream) -> uint8 tensor; each thread has its own, since the two kernels of one
+    call may be enqueued around those of another thread's call on the same stream."""
+
+    def __init__(self):
+        self.of = {}
+
+
+_ATTN_WORKSPACES = _Workspaces()
 
 
 def _workspace_size(fn: str, *shape) -> int:
@@ -729,8 +740,8 @@ def _workspace_size(fn: str, *shape) -> int:
 
 def _attn_workspace(fn: str, index: int, stream, *shape):
     """A workspace for a call of this shape on `stream` of GPU `index`, kept and reused by later
-    calls there; None where none is needed.  While a graph is being captured a new one is made
-    instead, in the graph's own memory, so that no two graphs share one."""
+    calls of this thread there; None where none is needed.  While a graph is being captured a new
+    one is made instead, in the graph's own memory, so that no two graphs share one."""
     need = _ATTN_SIZES.get((fn, index, shape))
     if need == 0:
         return None
@@ -748,10 +759,10 @@ def _attn_workspace(fn: str, index: int, stream, *shape):
     if torch._C._cuda_isCurrentStreamCapturing():
         return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
     key = (index, torch._C._cuda_getCurrentRawStream(index))
-    ws = _ATTN_WORKSPACES.get(key)
+    ws = _ATTN_WORKSPACES.of.get(key)
     if ws is None or ws.numel() < need:
-        ws = _ATTN_WORKSPACES[key] = torch.empty(need, dtype=torch.uint8,
-                                                 device=torch.device("cuda", index))
+        ws = _ATTN_WORKSPACES.of[key] = torch.empty(need, dtype=torch.uint8,
+                                                    device=torch.device("cuda", index))
     return ws
 
 
@@ -773,7 +784,7 @@ def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q
     sequences of keys put the queries at their end).  softmax_scale: head_dim ** -0.5 when None.
     Rows outside every sequence are left as they were (zeros when allocated here); lse, if given,
     is fp32 [tokens, Hq].  workspace: uint8, attn_prefill_workspace_size's bytes, for one call at a
-    time; by default one kept per stream by this module."""
+    time; by default one kept per thread and stream."""
     tq, qs = _head_rows(q, "q", num_q_heads, head_dim)
     tk, ks = _head_rows(k, "k", num_kv_heads, head_dim)
     tv, vs = _head_rows(v, "v", num_kv_heads, head_dim)
@@ -824,7 +835,7 @@ def fp8_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     block_tables [num_seqs, max_blocks] and context_lens [num_seqs] (the token's own position
     included, written before).  softmax_scale: head_dim ** -0.5 when None; lse, if given, is fp32
     [num_seqs, Hq].  workspace: uint8, fp8_attn_decode_workspace_size's bytes, for one call
-    at a time; by default one kept per stream by this module."""
+    at a time; by default one kept per thread and stream."""
     n, qs = _head_rows(q, "q", num_q_heads, head_dim)
     cs = block_size * num_kv_heads * head_dim if cache_stride is None else cache_stride
     blocks = _kv_num_blocks(k_cache, v_cache, cs)

@@ -1,10 +1,13 @@
 """GPU: the operators in a row as a layer uses them -- W8A8 projections, head norms with rotary
 positions and the paged write, attention over the prompt, then single-token steps over the cache,
 and a second chunk behind the history read back from it."""
+import threading
+
 import pytest
 import torch
 
 import fp8_e4m3_quantization_amd as fq
+from fp8_e4m3_quantization_amd import _lib
 from tests import attn_ref
 from tests.gpu_util import DEV, need_gpu
 
@@ -93,3 +96,47 @@ def test_prompt_then_steps_then_a_second_chunk():
                           HKV, D, lse=lse,
                           cu_seqlens_k=torch.tensor([0, n + more], dtype=torch.int32, device=DEV))
     attn_ref.prefill(qo, kall, vall, [0, more], [0, n + more], HQ, HKV, D, D ** -0.5, True, out, lse)
+
+
+def test_two_threads_on_one_stream():
+    """Each thread's calls enqueue two kernels with a workspace between them; calls of another
+    thread on the same stream may come in between."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    hq, hkv, d, bs, n = 16, 2, 128, 16, 3000
+    blocks = n // bs + 1
+    kc, vc = ((torch.randn((blocks * bs * hkv * d,), generator=g, device=DEV)).to(torch.float8_e4m3fn)
+              .view(torch.uint8) for _ in range(2))
+    tables = torch.randperm(blocks, generator=g, device=DEV).to(torch.int32)[None]
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    cu_q = torch.tensor([0, 20], dtype=torch.int32, device=DEV)
+    cu_k = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    k, v = (torch.randn((n, hkv * d), generator=g, device=DEV).to(BF16) for _ in range(2))
+    qs = [torch.randn((20, hq * d), generator=g, device=DEV).to(BF16) for _ in range(2)]
+    assert fq.attn_prefill_workspace_size(1, 20, n, hq, hkv, d) > 0
+
+    def calls(q):
+        return (fq.fp8_attn_decode(q[:1], kc, vc, tables, lens, hq, hkv, d, bs, 1.0, 1.0),
+                fq.attn_prefill(q, k, v, cu_q, hq, hkv, d, cu_seqlens_k=cu_k))
+
+    want = [calls(q) for q in qs]
+    got = [[], []]
+    spaces = [None, None]
+    start = threading.Barrier(2)
+
+    def work(i):
+        start.wait()
+        for _ in range(200):
+            got[i].append(calls(qs[i]))
+        spaces[i] = [t.data_ptr() for t in _lib._ATTN_WORKSPACES.of.values()]
+        start.wait()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert spaces[0] and spaces[1] and not set(spaces[0]) & set(spaces[1])
+    for i in range(2):
+        assert len(got[i]) == 200
+        for pair in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(pair, want[i]))
