@@ -451,15 +451,20 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
     if constexpr (D == 128) pair_up<D>();
     move_to(top, next);
   };
-  auto mask = [&](int t, v16f* s) {
-    const int left = limit - t * kTileKeys - 4 * half;
+  // The scores of tile t, which may be seen in part.
+  auto scores = [&](int t, v16f* s, const uint16_t* kt) {
+    products(s, kt);
+    if (t >= my_whole) {
+      const int left = limit - t * kTileKeys - 4 * half;
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        s[b][r] = 32 * b + 8 * (r >> 2) + (r & 3) < left ? s[b][r] : neg_inf();
-        if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // few conditions alive at a time
-      }
+        for (int r = 0; r < 16; ++r) {
+          s[b][r] = 32 * b + 8 * (r >> 2) + (r & 3) < left ? s[b][r] : neg_inf();
+          if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // few conditions alive at a time
+        }
+    }
+    move_to(largest(s), s);
   };
   if (tiles > 0) {
     v16f sa[2];
@@ -467,11 +472,7 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
     copy_next(vsrc, v0);
     copy_next(ksrc, k1);
     landed();
-    if (my_tiles > 0) {
-      products(sa, k0);
-      if (my_whole == 0) mask(0, sa);
-      move_to(largest(sa), sa);
-    }
+    if (my_tiles > 0) scores(0, sa, k0);
     int t = 0;
     for (; t + 2 < my_whole; t += 2) {
       v16f sb[2];
@@ -484,11 +485,7 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
       next_tile(kt, t & 1 ? v0 : v1);
 #pragma unroll
       for (int st = 0; st < 4; ++st) odd |= add_values(vt, st, weights(sa, st), std::true_type{});
-      if (t + 1 < my_tiles) {
-        products(sa, t & 1 ? k0 : k1);
-        if (t + 1 >= my_whole) mask(t + 1, sa);
-        move_to(largest(sa), sa);
-      }
+      if (t + 1 < my_tiles) scores(t + 1, sa, t & 1 ? k0 : k1);
     }
     for (; t < tiles; ++t) next_tile(t & 1 ? k1 : k0, t & 1 ? v0 : v1);
   }
