@@ -13,7 +13,9 @@
 // 4g..4g+3 and 16+4g..16+4g+3 of the tile, which are taken as its 8 of the 32 summed by the
 // second product as they lie; it loads V at the same 8 positions, bytes D/16 (l % 16) onwards,
 // so that both operands agree without an exchange.  P is rounded to bf16 for that product (at
-// most 2^-9 of each weight, under the output's own rounding).
+// most 2^-9 of each weight, under the output's own rounding); out's denominator is the sum of the
+// rounded weights (one more row of the product, of ones), so that a weight that outweighs all
+// others loses nothing by its rounding; lse is of the unrounded ones.
 //
 // The histories of all sequences, laid end to end, are cut into equal shares, one for each CU,
 // whatever the lengths.  A workgroup's waves take the KV heads of its share side by side (a
@@ -46,7 +48,7 @@ struct DecodeArgs {
   uint16_t* out;
   float* lse;
   float* parts;      // [2 * shares][heads of work][rows_most][D]: sums of weighted values
-  float2* stats;     // [2 * shares][heads of work][rows_most]: reference, sum of weights
+  float4* stats;     // [2 * shares][heads of work][rows_most]: Sums' values
   int64_t ts, qs, os, cs, nblocks;
   int seqs, width, hq, hkv, group, bs;
   int row_tiles;     // ceil(group / 16)
@@ -62,20 +64,22 @@ __device__ __forceinline__ int seq_len(const DecodeArgs& a, int s) {
   return min(max(n, 0), a.width * a.bs);
 }
 
-// Sums of weights and of weighted values against a reference, and how two of them add up.
-struct Partial {
-  float ref, total;
-  float4 v;
+// Sums of weights against a reference, and how two of them add up: by factors f and h, which
+// hold for their weighted values too.
+struct Sums {
+  float ref, total, rounded;  // reference (log2 units), sums of the weights and of the rounded ones
+  __device__ __forceinline__ Sums(float r, float t, float s) : ref(r), total(t), rounded(s) {}
+  __device__ __forceinline__ explicit Sums(float4 x) : ref(x.x), total(x.y), rounded(x.z) {}
+  __device__ __forceinline__ float4 packed() const { return make_float4(ref, total, rounded, 0.0f); }
+  __device__ __forceinline__ void add(const Sums& b, float* f, float* h) {
+    const float to = fmaxf(ref, b.ref);
+    *f = ref == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(ref - to);
+    *h = b.ref == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(b.ref - to);
+    ref = to;
+    total = total * *f + b.total * *h;
+    rounded = rounded * *f + b.rounded * *h;
+  }
 };
-__device__ __forceinline__ void add_to(Partial& a, const Partial& b) {
-  const float to = fmaxf(a.ref, b.ref);
-  const float f = a.ref == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(a.ref - to);
-  const float h = b.ref == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(b.ref - to);
-  a.total = a.total * f + b.total * h;
-  a.v.x = a.v.x * f + b.v.x * h; a.v.y = a.v.y * f + b.v.y * h;
-  a.v.z = a.v.z * f + b.v.z * h; a.v.w = a.v.w * f + b.v.w * h;
-  a.ref = to;
-}
 
 // Two E4M3 codes (low or high half of w) as two bf16, exact.
 template <bool kHigh>
@@ -149,9 +153,9 @@ __device__ __forceinline__ Cut cut_up(const DecodeArgs& a, int waves, FirstSeqs*
 
 // Stores N values (4 or more) of query head `head`, from d on; the first lane of a row its lse.
 template <int D, int N>
-__device__ __forceinline__ void finish(const DecodeArgs& a, int seq, int head, int d, float ref,
-                                       float total, const float* v) {
-  const float inv = total == 0.0f ? 0.0f : a.v_scale / total;
+__device__ __forceinline__ void finish(const DecodeArgs& a, int seq, int head, int d, const Sums& s,
+                                       const float* v) {
+  const float inv = s.total == 0.0f ? 0.0f : a.v_scale / s.rounded;
   uint16_t* to = a.out + seq * a.os + int64_t(head) * D + d;
 #pragma unroll
   for (int i = 0; i < N; i += 4)
@@ -159,7 +163,7 @@ __device__ __forceinline__ void finish(const DecodeArgs& a, int seq, int head, i
                                                    cvt_bf16x2(v[i + 2] * inv, v[i + 3] * inv));
   if (a.lse && d == 0)
     a.lse[int64_t(seq) * a.hq + head] =
-        total == 0.0f ? neg_inf() : (ref + __builtin_amdgcn_logf(total)) * kLn2;
+        s.total == 0.0f ? neg_inf() : (s.ref + __builtin_amdgcn_logf(s.total)) * kLn2;
 }
 
 // Waves of a workgroup: 256-wide heads need twice the registers.
@@ -212,7 +216,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D == 256 ? 1 : 2) void decode_kerne
 
   __shared__ int64_t s_row[kDecWaves][kDecTile];
   __shared__ __attribute__((aligned(16))) v4f s_o[kDecWaves][kOut][64];
-  __shared__ float2 s_stats[kDecWaves][64];
+  __shared__ __attribute__((aligned(16))) float4 s_stats[kDecWaves][64];
   const int64_t e = int64_t(a.hkv) * D;
 
   while (true) {  // over the share's pieces of sequences
@@ -265,6 +269,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D == 256 ? 1 : 2) void decode_kerne
   v4f o[kOut];
 #pragma unroll
   for (int i = 0; i < kOut; ++i) o[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  v4f ones_row = {0.0f, 0.0f, 0.0f, 0.0f};  // sums of the rounded weights, the same in each row
   float ref = neg_inf(), sum = 0.0f;
   float sc[8];
   auto scores = [&]() {
@@ -293,6 +298,7 @@ __global__ __launch_bounds__(64 * kDecWaves, D == 256 ? 1 : 2) void decode_kerne
       const float f = moves ? __builtin_amdgcn_exp2f(ref - top) : 1.0f;
       ref = moves ? top : ref;
       sum *= f;
+      ones_row *= f;
 #pragma unroll
       for (int i = 0; i < kOut; ++i) o[i] *= f;
     }
@@ -305,6 +311,8 @@ __global__ __launch_bounds__(64 * kDecWaves, D == 256 ? 1 : 2) void decode_kerne
       pw[j / 2] = cvt_bf16x2(x, y);
     }
     const v8bf pf = __builtin_bit_cast(v8bf, v4u{pw[0], pw[1], pw[2], pw[3]});
+    const v8bf ones = __builtin_bit_cast(v8bf, v4u{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
+    ones_row = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, pf, ones_row, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < kOut; i += 2) {  // values i and i + 1 of each lane's D/16
       uint32_t pair[8];
@@ -349,24 +357,20 @@ __global__ __launch_bounds__(64 * kDecWaves, D == 256 ? 1 : 2) void decode_kerne
   }
 
   // o[i][r] is value kOut (4g + r) + i of query column l % 16.
-  sum = sum_over_rows(sum);
+  Sums sums(ref, sum_over_rows(sum), ones_row[0]);
   // The waves of a head add up in pairs, the later half leaving its registers in LDS for the
   // earlier one, which holds the same values of the same queries.
   for (int half = turns / 2; half >= 1; half /= 2) {
     if (turn >= half && turn < 2 * half) {
 #pragma unroll
       for (int i = 0; i < kOut; ++i) s_o[wave][i][lane] = o[i];
-      s_stats[wave][lane] = make_float2(ref, sum);
+      s_stats[wave][lane] = sums.packed();
     }
     __syncthreads();
     if (turn < half) {
       const int from = wave + half * a.together;
-      const float2 st = s_stats[from][lane];
-      const float to = fmaxf(ref, st.x);
-      const float f = ref == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(ref - to);
-      const float h = st.x == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(st.x - to);
-      ref = to;
-      sum = sum * f + st.y * h;
+      float f, h;
+      sums.add(Sums(s_stats[from][lane]), &f, &h);
 #pragma unroll
       for (int i = 0; i < kOut; ++i) o[i] = o[i] * f + s_o[from][i][lane] * h;
     }
@@ -380,12 +384,12 @@ __global__ __launch_bounds__(64 * kDecWaves, D == 256 ? 1 : 2) void decode_kerne
 #pragma unroll
       for (int i = 0; i < kOut; ++i) v[i] = o[i][r];
       if (sp.parts == 1) {
-        finish<D, kOut>(a, seq, head_of(hw) + col, d, ref, sum, v);
+        finish<D, kOut>(a, seq, head_of(hw) + col, d, sums, v);
       } else {
 #pragma unroll
         for (int i = 0; i < kOut; i += 4)
           *reinterpret_cast<float4*>(a.parts + at * D + d + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        if (d == 0) a.stats[at] = make_float2(ref, sum);
+        if (d == 0) a.stats[at] = sums.packed();
       }
     }
   }
@@ -418,10 +422,17 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const DecodeArgs a, 
   const int kvh = head / a.group, of_group = head - kvh * a.group;
   const int hw = kvh * a.row_tiles + of_group / kDecRows, r = of_group % kDecRows;
   const int slot = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
-  Partial sum = {neg_inf(), 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+  Sums sums(neg_inf(), 0.0f, 0.0f);
+  float4 all = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  auto add = [&](const Sums& b, float4 x) {
+    float f, h;
+    sums.add(b, &f, &h);
+    all.x = all.x * f + x.x * h; all.y = all.y * f + x.y * h;
+    all.z = all.z * f + x.z * h; all.w = all.w * f + x.w * h;
+  };
   for (int c = slot; c < sp.parts; c += kSlots * kJoinAtOnce) {
     float4 v[kJoinAtOnce];
-    float2 st[kJoinAtOnce];
+    float4 st[kJoinAtOnce];
 #pragma unroll
     for (int j = 0; j < kJoinAtOnce; ++j) {
       const int part = min(c + j * kSlots, sp.parts - 1);
@@ -431,19 +442,19 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const DecodeArgs a, 
     }
 #pragma unroll
     for (int j = 0; j < kJoinAtOnce; ++j)
-      if (c + j * kSlots < sp.parts) add_to(sum, Partial{st[j].x, st[j].y, v[j]});
+      if (c + j * kSlots < sp.parts) add(Sums(st[j]), v[j]);
   }
   __shared__ __attribute__((aligned(16))) float s_v[kSlots][D];
-  __shared__ float2 s_st[kSlots];
-  *reinterpret_cast<float4*>(&s_v[slot][d]) = sum.v;
-  if (d == 0) s_st[slot] = make_float2(sum.ref, sum.total);
+  __shared__ __attribute__((aligned(16))) float4 s_st[kSlots];
+  *reinterpret_cast<float4*>(&s_v[slot][d]) = all;
+  if (d == 0) s_st[slot] = sums.packed();
   __syncthreads();
   if (slot > 0) return;
 #pragma unroll
   for (int u = 1; u < kSlots; ++u)
-    add_to(sum, Partial{s_st[u].x, s_st[u].y, *reinterpret_cast<const float4*>(&s_v[u][d])});
-  const float v[4] = {sum.v.x, sum.v.y, sum.v.z, sum.v.w};
-  finish<D, 4>(a, seq, head, d, sum.ref, sum.total, v);
+    add(Sums(s_st[u]), *reinterpret_cast<const float4*>(&s_v[u][d]));
+  const float v[4] = {all.x, all.y, all.z, all.w};
+  finish<D, 4>(a, seq, head, d, sums, v);
 }
 
 int decode_shape(int32_t seqs, int32_t hq, int32_t hkv, int32_t d) {
@@ -480,7 +491,7 @@ DecodePlan decode_plan(int32_t hq, int32_t hkv, int32_t d, int32_t seqs, int64_t
   if (p.shares < 8) p.shares = 8;
   const uint64_t rows = uint64_t(2 * p.shares) * p.heads * p.rows;
   p.parts_bytes = rows * d * 4;
-  p.bytes = p.parts_bytes + rows * 8;
+  p.bytes = p.parts_bytes + rows * 16;
   return p;
 }
 
@@ -546,7 +557,7 @@ extern "C" int fp8_attn_decode(const uint16_t* q, const uint8_t* k_cache, const 
   a.bs = block_size, a.row_tiles = p.row_tiles, a.heads = p.heads, a.together = p.together;
   a.shares = p.shares, a.rows_most = p.rows;
   a.parts = static_cast<float*>(workspace);
-  a.stats = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.parts_bytes);
+  a.stats = reinterpret_cast<float4*>(static_cast<uint8_t*>(workspace) + p.parts_bytes);
   a.scale_log2 = softmax_scale * k_scale * kLog2e;
   a.v_scale = v_scale;
   const int64_t blocks = (p.shares > 0 ? int64_t(p.shares) : (int64_t(num_seqs) + 7) / 8 * 8) *

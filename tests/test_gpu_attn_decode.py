@@ -184,6 +184,30 @@ def test_huge_scores_pick_the_largest(lens, unit):
             attn_ref.check(lse[i, h], want, 5 * attn_ref.U24 * want.abs() + 2.0 ** -20, "lse")
 
 
+def test_one_weight_above_all_others():
+    """One position outweighs one other by 2^x, 0.5 <= x < 8, behind it in the same wave, so that
+    its weight against the running reference is 2^x and is rounded to bf16.  The rounding, by a
+    factor 1 + e with |e| <= 2^-8, is in numerator and denominator: with w the true share and V = 0
+    at the other position, out = V w (1 + e) / (1 + w e) is off by at most V w (1 - w) 2^-8 (1 + 2^-7),
+    and by its own rounding and a few binary32 steps."""
+    n, d, bs, seqs, at = 300, 64, 4, 64, 256
+    kc = torch.full((75, bs, d), -448.0, device=DEV)
+    vc = torch.zeros((75, bs, d), device=DEV)
+    kc[0, 0] = 0.0
+    kc[at // bs, 0] = 1.0
+    vc[at // bs, 0] = torch.arange(1, d + 1, device=DEV) * 4.0
+    kc, vc = (x.to(torch.float8_e4m3fn).view(torch.uint8).reshape(-1) for x in (kc, vc))
+    c = (torch.linspace(0.5, 7.9, seqs, device=DEV) * math.log(2) / d).to(BF16)
+    q = c[:, None].expand(seqs, d).contiguous()
+    tables = torch.arange(75, dtype=torch.int32, device=DEV).repeat(seqs, 1)
+    lens = torch.full((seqs,), n, dtype=torch.int32, device=DEV)
+    out = fq.fp8_attn_decode(q, kc, vc, tables, lens, 1, 1, d, bs, 1.0, 1.0, softmax_scale=1.0)
+    w = torch.sigmoid(c.double() * d)[:, None]
+    v = attn_ref.e4m3_values(vc).view(-1, d)[at]
+    bound = attn_ref.HALF_BF16 * w * v + 2.0 ** -8 * (1 + 2.0 ** -7) * w * (1 - w) * v + 2.0 ** -18 * v
+    attn_ref.check(out, w * v, bound, "out")
+
+
 def test_cache_past_four_gib():
     """Blocks whose byte offsets pass 2^32."""
     bs, hkv, d = 16, 4, 128
