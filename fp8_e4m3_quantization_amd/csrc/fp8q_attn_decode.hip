@@ -22,6 +22,9 @@
 // token's heads lie side by side in the pools) and, with fewer heads than waves, its tiles in
 // turn.  A sequence that lies in several shares leaves their sums in the workspace, and a second
 // kernel adds them in the sequence's order: results do not depend on the order of workgroups.
+// One workgroup a CU: more read no faster.  Measured: 64 sequences of 500 to 8100 positions, 8 KV
+// heads of 128 (525 MB): 95 us and 6 for the join, 5.5 TB/s; 2 of 131072 and 100003, 4 KV heads:
+// 46 us and 7, 5.2 TB/s (a plain read stream: 5.9-6.2).
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>

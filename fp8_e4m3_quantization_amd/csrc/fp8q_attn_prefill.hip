@@ -14,6 +14,15 @@
 // order 4h..4h+3, 8+4h..8+4h+3 for lane half h; V^T comes from LDS in that order through the
 // transposing 8-byte LDS read.  P is rounded to bf16 for that product (at most 2^-9 of each
 // weight, under the output's own rounding); the sum of weights is of the unrounded ones.
+//
+// Bound: matrix cores and vector ALUs alike (a score costs as long in its exponential as in its
+// products at 128-wide heads), two waves of a SIMD overlapping them: 4593 queries of 40 heads,
+// 4 KV heads, 128 wide, causal (217 GFLOP) take 226 us, 960 TFLOP/s, at a clock of 1.85 GHz under
+// that load; matrix cores are busy 55 % and vector ALUs 51 % of the time, LDS 27 % without
+// conflicts.  The products and copies alone take 166 us, with the softmax 190.  128 queries a
+// workgroup: 32 a wave, since o, two tiles of scores and q fill the registers of two waves a SIMD
+// (64 a wave, alone on its SIMD: 320 us).  64-wide heads: three waves a SIMD, two prompts of 2500 in
+// 72 us, vector ALUs busy 69 %.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>

@@ -353,7 +353,8 @@ int fp8_kv_amax(const uint16_t* k, const uint16_t* v, int64_t n_elems, float* am
  * fp8_qk_norm_rope_kv_write also writes the caches as fp8_kv_write(k_out, v, ...) would (the
  * same bytes: the codes are made of the rounded bf16 keys, so that a calibration window's replay
  * of staged rows leaves what the live write leaves); a token whose slot is outside the pool gets
- * its q_out (and k_out) and no cache write.
+ * its q_out (and k_out) and no cache write.  Where tokens of one call share a slot, each of its
+ * bytes is one of theirs, of which is not defined.
  *   q, k, v        device bf16 rows of H*D values at q_stride / key_stride / value_stride
  *                  (views of one projection's output are fine)
  *   q_weight, k_weight  device bf16 [D] or NULL;  0 <= eps <= 1
@@ -412,6 +413,7 @@ int fp8_qk_norm_rope_kv_write(const uint16_t* q, const uint16_t* k, const uint16
  * Few queries over long keys are split along the keys: then two kernels are enqueued, the second
  * joining the parts in order, and a workspace is needed (results do not depend on the order in
  * which workgroups run).  attn_prefill_workspace_size: for the current device.
+ * The scores must stay within binary32.  Outputs must not overlap inputs.
  * Errors: FP8Q_EINVAL, FP8Q_ENULL, FP8Q_EALIGN, FP8Q_ELAUNCH. */
 int attn_prefill_workspace_size(int32_t num_seqs, int32_t total_q, int32_t total_k,
                                 int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
@@ -449,7 +451,9 @@ int attn_prefill(const uint16_t* q, const uint16_t* k, const uint16_t* v,
  *   max_blocks * block_size <= 2^30 and num_seqs * (max_blocks * block_size / 32 + 1) <= 2^30;
  *   cache_stride >= block_size*H*D, a multiple of 16; q / out
  *   strides multiples of 8; k_scale, v_scale in [2^-64, 2^64]; 0 < softmax_scale <= 2^32.
- * Enqueues two kernels (the second joins the parts of long histories).
+ * The scores must stay within binary32.  Outputs must not overlap inputs.
+ * Enqueues two kernels where max_blocks * block_size > 1024 (the second joins the parts of
+ * histories that were cut), else one.
  * fp8_attn_decode_workspace_size: for the current device.
  * Errors: FP8Q_EINVAL, FP8Q_ENULL, FP8Q_EALIGN, FP8Q_ELAUNCH. */
 int fp8_attn_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
