@@ -444,11 +444,30 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
     copy_next(ksrc, k_free);
     copy_next(vsrc, v_free);
   };
-  // One turn of the pipeline, for tiles that the wave sees whole: the scores of tile t + 1 (matrix
+  auto mask = [&](int t, v16f* s) {
+    const int left = limit - t * kTileKeys - 4 * half;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        s[b][r] = 32 * b + 8 * (r >> 2) + (r & 3) < left ? s[b][r] : neg_inf();
+        if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // few conditions alive at a time
+      }
+  };
+  // The scores of tile t, which may be seen in part.
+  auto scores = [&](int t, v16f* s, const uint16_t* kt) {
+    products(s, kt);
+    if (t >= my_whole) {
+      mask(t, s);
+    }
+    move_to(largest(s), s);
+  };
+  // One turn of the pipeline, for a tile t that the wave sees whole: the scores of tile t + 1 (matrix
   // cores) beside the weights of tile t (vector ALUs), then tile t's values (matrix cores) beside
-  // the largest of the new scores.
+  // the largest of the new scores.  `part`: std::false_type where tile t + 1 is seen whole too, else
+  // t + 1, whose scores are masked behind the products (in between, the registers do not suffice).
   auto turn = [&](const v16f* s, v16f* next, const uint16_t* kn, const uint16_t* vt,
-                  uint16_t* k_free, uint16_t* v_free) {
+                  uint16_t* k_free, uint16_t* v_free, auto part) {
     next_tile(k_free, v_free);
     products(next, kn);
     v8bf p[4];
@@ -456,24 +475,16 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
     for (int st = 0; st < 4; ++st) p[st] = weights(s, st);
 #pragma unroll
     for (int st = 0; st < 4; ++st) add_values(vt, st, p[st], std::false_type{});
-    const float top = largest(next);
-    if constexpr (D == 128) pair_up<D>();
-    move_to(top, next);
-  };
-  // The scores of tile t, which may be seen in part.
-  auto scores = [&](int t, v16f* s, const uint16_t* kt) {
-    products(s, kt);
-    if (t >= my_whole) {
-      const int left = limit - t * kTileKeys - 4 * half;
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          s[b][r] = 32 * b + 8 * (r >> 2) + (r & 3) < left ? s[b][r] : neg_inf();
-          if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // few conditions alive at a time
-        }
+    if constexpr (std::is_same<decltype(part), std::false_type>::value) {
+      const float top = largest(next);
+      if constexpr (D == 128) pair_up<D>();
+      move_to(top, next);
+    } else {
+      if constexpr (D == 128) pair_up<D>();
+      __builtin_amdgcn_sched_barrier(0);
+      mask(part, next);
+      move_to(largest(next), next);
     }
-    move_to(largest(s), s);
   };
   if (tiles > 0) {
     v16f sa[2];
@@ -485,8 +496,18 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
     int t = 0;
     for (; t + 2 < my_whole; t += 2) {
       v16f sb[2];
-      turn(sa, sb, k1, v0, k0, v1);
-      turn(sb, sa, k0, v1, k1, v0);
+      turn(sa, sb, k1, v0, k0, v1, std::false_type{});
+      turn(sb, sa, k0, v1, k1, v0, std::false_type{});
+    }
+    if (t < my_whole && t + 1 < my_tiles) {
+      v16f sb[2];
+      turn(sa, sb, k1, v0, k0, v1, ++t);
+      if (t < my_whole && t + 1 < my_tiles) {
+        turn(sb, sa, k0, v1, k1, v0, ++t);
+      } else {
+        sa[0] = sb[0];
+        sa[1] = sb[1];
+      }
     }
     first_held = t;
     for (; t < my_tiles; ++t) {  // the last tiles, among them those that are seen in part
