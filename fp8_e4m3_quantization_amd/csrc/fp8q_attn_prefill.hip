@@ -72,20 +72,19 @@ __device__ __forceinline__ void seq_span(const int32_t* cu, int s, int total, in
 
 // The sequence and row tile (of `rows` queries) of work item `rank`, or false.  Tiles are ranked
 // by descending index within their sequence (under a causal mask a later tile has more keys), so
-// that the longest run first and the short ones fill the last round.
-__device__ __forceinline__ bool find_tile(const PrefillArgs& a, int rows, int rank, int* seq,
-                                          int* tile) {
+// that the longest run first and the short ones fill the last round.  `first`: the length of
+// sequence `lane`, of the first 64.
+__device__ __forceinline__ bool find_tile(const PrefillArgs& a, int rows, int rank, int first,
+                                          int* seq, int* tile) {
   const int lane = threadIdx.x & 63;
   auto tiles_of = [&](int s) {
-    int st, n = 0;
-    if (s < a.seqs) seq_span(a.cu_q, s, a.tq, &st, &n);
+    int st, n = s < 64 ? first : 0;
+    if (s >= 64 && s < a.seqs) seq_span(a.cu_q, s, a.tq, &st, &n);
     return (n + rows - 1) / rows;
   };
   if (a.seqs == 1) {
-    int st, n;
-    seq_span(a.cu_q, 0, a.tq, &st, &n);
     *seq = 0;
-    *tile = (n + rows - 1) / rows - 1 - rank;
+    *tile = __builtin_amdgcn_readlane(tiles_of(lane), 0) - 1 - rank;
     return *tile >= 0;
   }
   if (a.seqs > kOrderedSeqs) {  // in sequence order
@@ -104,17 +103,11 @@ __device__ __forceinline__ bool find_tile(const PrefillArgs& a, int rows, int ra
     return false;
   }
   int n[kOrderedSeqs / 64];
-  int most = 0;
 #pragma unroll
-  for (int c = 0; c < kOrderedSeqs / 64; ++c) {
-    n[c] = c * 64 < a.seqs ? tiles_of(c * 64 + lane) : 0;
-    most = max(most, n[c]);
-  }
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) most = max(most, __shfl_xor(most, o));
+  for (int c = 0; c < kOrderedSeqs / 64; ++c) n[c] = c * 64 < a.seqs ? tiles_of(c * 64 + lane) : 0;
   // S(L) = number of tiles with index >= L; find the largest L with S(L) > rank, 64 candidates
   // at a time (one per lane)
-  int lo = 0, hi = most;  // S(lo) > rank is wanted, S(hi) = 0
+  int lo = 0, hi = (a.tq + rows - 1) / rows;  // S(lo) > rank is wanted, S(hi) = 0
   auto at_least = [&](int level) {
     int sum = 0;
 #pragma unroll
@@ -176,12 +169,25 @@ __device__ __forceinline__ bool find_item(const PrefillArgs& a, int index, Item*
     it->head = index % a.hq;
     rank = index / a.hq;
   }
-  int seq, tile;
-  if (!find_tile(a, kPrefillRows, rank, &seq, &tile)) return false;
+  // where the first 64 sequences lie, one to a lane: read at once, before the search
+  const int lane = threadIdx.x & 63;
+  int q0 = 0, lq = 0, kv0 = 0, lk = 0, seq, tile;
+  if (lane < a.seqs) {
+    seq_span(a.cu_q, lane, a.tq, &q0, &lq);
+    seq_span(a.cu_k, lane, a.tk, &kv0, &lk);
+  }
+  if (!find_tile(a, kPrefillRows, rank, lq, &seq, &tile)) return false;
   it->seq = __builtin_amdgcn_readfirstlane(seq);
   it->tile = __builtin_amdgcn_readfirstlane(tile);
-  seq_span(a.cu_q, it->seq, a.tq, &it->q0, &it->lq);
-  seq_span(a.cu_k, it->seq, a.tk, &it->kv0, &it->lk);
+  if (it->seq < 64) {
+    it->q0 = __builtin_amdgcn_readlane(q0, it->seq);
+    it->lq = __builtin_amdgcn_readlane(lq, it->seq);
+    it->kv0 = __builtin_amdgcn_readlane(kv0, it->seq);
+    it->lk = __builtin_amdgcn_readlane(lk, it->seq);
+  } else {
+    seq_span(a.cu_q, it->seq, a.tq, &it->q0, &it->lq);
+    seq_span(a.cu_k, it->seq, a.tk, &it->kv0, &it->lk);
+  }
   return true;
 }
 
