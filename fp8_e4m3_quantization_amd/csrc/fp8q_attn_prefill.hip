@@ -17,12 +17,11 @@
 //
 // Bound: matrix cores and vector ALUs alike (a score costs as long in its exponential as in its
 // products at 128-wide heads), two waves of a SIMD overlapping them: 4593 queries of 40 heads,
-// 4 KV heads, 128 wide, causal (217 GFLOP) take 226 us, 960 TFLOP/s, at a clock of 1.85 GHz under
-// that load; matrix cores are busy 55 % and vector ALUs 51 % of the time, LDS 27 % without
-// conflicts.  The products and copies alone take 166 us, with the softmax 190.  128 queries a
+// 4 KV heads, 128 wide, causal (217 GFLOP) take 217 us, 1.0 PFLOP/s, at a clock of 1.85 GHz under
+// that load; matrix cores are busy 56 % and vector ALUs 51 % of the time, LDS 29 %.  The products and copies alone take 166 us, with the softmax 190.  128 queries a
 // workgroup: 32 a wave, since o, two tiles of scores and q fill the registers of two waves a SIMD
 // (64 a wave, alone on its SIMD: 320 us).  64-wide heads: three waves a SIMD, two prompts of 2500 in
-// 72 us, vector ALUs busy 69 %.
+// 67 us, vector ALUs busy 72 %.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -627,7 +626,7 @@ __global__ __launch_bounds__(kPrefillJoinThreads) void prefill_join_kernel(const
 // are split into: the number with the least estimated time.  A workgroup alone on its CU takes
 // about 1 us a tile of 64 keys (128-wide heads), two on one CU about 2; joining parts costs a
 // launch and the way of their sums through memory.  512 queries of 40 heads over 8704 keys: 144 us
-// in one part, 111 in three; 23 queries over 2794 keys, 10 heads: 44 us in one, 17 in eleven.
+// in one part, 101 in three; 23 queries over 2794 keys, 10 heads: 44 us in one, 17 in eleven.
 struct PrefillPlan {
   int64_t items;
   int parts;
