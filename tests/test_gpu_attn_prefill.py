@@ -220,3 +220,49 @@ def test_another_stream_and_a_replayed_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+def test_rows_past_four_gib():
+    """Rows 8 MiB apart: the last lie 5.5 GiB behind the first."""
+    n, hq, hkv, d = 700, 2, 1, 128
+    g = torch.Generator(device=DEV).manual_seed(5)
+    wide = torch.empty((n, 1 << 22), dtype=BF16, device=DEV)
+    cols = [0, 256, 384, 512]
+    q, k, v, out = (wide[:, c:c + w] for c, w in zip(cols, (256, 128, 128, 256)))
+    for t in (q, k, v):
+        t.copy_(torch.randn(t.shape, generator=g, device=DEV))
+    starts = [0, 30, n]
+    cu = torch.tensor(starts, dtype=torch.int32, device=DEV)
+    lse = torch.empty((n, hq), device=DEV)
+    fq.attn_prefill(q, k, v, cu, hq, hkv, d, out=out, lse=lse)
+    attn_ref.prefill(q, k, v, starts, starts, hq, hkv, d, d ** -0.5, True, out, lse)
+
+
+def test_two_graphs_of_split_calls():
+    """Each graph has its own sums, whichever order they are replayed in, beside eager calls."""
+    hq, hkv, d, lk = 8, 2, 128, 3000
+    g = torch.Generator(device=DEV).manual_seed(6)
+    cu_k = torch.tensor([0, lk], dtype=torch.int32, device=DEV)
+    k, v = (torch.randn((lk, hkv * d), generator=g, device=DEV).to(BF16) for _ in range(2))
+    calls = []
+    for lq in (20, 33):
+        assert fq.attn_prefill_workspace_size(1, lq, lk, hq, hkv, d) > 0
+        q = torch.randn((lq, hq * d), generator=g, device=DEV).to(BF16)
+        cu = torch.tensor([0, lq], dtype=torch.int32, device=DEV)
+        want = fq.attn_prefill(q, k, v, cu, hq, hkv, d, cu_seqlens_k=cu_k)
+        out = torch.empty_like(want)
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            fq.attn_prefill(q, k, v, cu, hq, hkv, d, cu_seqlens_k=cu_k, out=out)
+        calls.append((q, cu, want, out, graph))
+    for order in ((0, 1), (1, 0), (0, 0), (1, 1)):
+        for _, _, _, out, _ in calls:
+            out.zero_()
+        for i in order:
+            calls[i][4].replay()
+        q, cu, want, _, _ = calls[order[0]]
+        assert torch.equal(fq.attn_prefill(q, k, v, cu, hq, hkv, d, cu_seqlens_k=cu_k), want)
+        torch.cuda.synchronize()
+        for i in set(order):
+            assert torch.equal(calls[i][3], calls[i][2])

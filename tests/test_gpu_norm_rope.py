@@ -165,3 +165,20 @@ def test_another_stream_and_a_replayed_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((qo, kc, vc), want))
+
+
+@pytest.mark.parametrize("d", [128, 96])
+def test_rows_past_four_gib(d):
+    """Rows 8 MiB apart give what packed rows give."""
+    t, hq, hkv = 600, 2, 1
+    g = torch.Generator(device=DEV).manual_seed(d)
+    wide = torch.empty((t, 1 << 22), dtype=torch.bfloat16, device=DEV)
+    q, k = wide[:, :hq * d], wide[:, 256:256 + hkv * d]
+    for x in (q, k):
+        x.copy_(torch.randn(x.shape, generator=g, device=DEV))
+    positions = torch.randint(0, 1000, (t,), generator=g, device=DEV)
+    table = torch.randn((1000, 32), generator=g, device=DEV)
+    want = fq.qk_norm_rope(q.contiguous(), k.contiguous(), positions, table, hq, hkv, d)
+    got = fq.qk_norm_rope(q, k, positions, table, hq, hkv, d, q_out=wide[:, 512:512 + hq * d],
+                          k_out=wide[:, 768:768 + hkv * d])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
