@@ -12,8 +12,10 @@
 // exchange but one between lanes l and l ^ 32.  The lane's 16 scores of a 32-key tile are then
 // the B operand of O^T += V^T P^T as they lie, when the keys of each 16-key step are taken in the
 // order 4h..4h+3, 8+4h..8+4h+3 for lane half h; V^T comes from LDS in that order through the
-// transposing 8-byte LDS read.  P is rounded to bf16 for that product (at most 2^-9 of each
-// weight, under the output's own rounding); the sum of weights is of the unrounded ones.
+// transposing 8-byte LDS read.  P is rounded to bf16 for that product (by up to 2^-8 of each
+// weight, as much as the output's own rounding); out's denominator is the sum of the rounded
+// weights, so that a weight that outweighs all others loses nothing by its rounding; lse is of the
+// unrounded ones.
 //
 // Bound: matrix cores and vector ALUs alike (a score costs as long in its exponential as in its
 // products at 128-wide heads), two waves of a SIMD overlapping them: 4593 queries of 40 heads,
@@ -53,7 +55,8 @@ struct PrefillArgs {
   int most_parts;    // parts of a tile's keys; 1: not split
   float scale_log2;  // softmax scale * log2(e)
   float* sums;       // [work items][parts][rows][D] where split
-  float2* stats;     // [work items][parts][rows]: reference (log2 units), sum of weights
+  float4* stats;     // [work items][parts][rows]: reference (log2 units), sums of the weights and
+                     // of the rounded ones
 };
 
 // Parts that `tiles` tiles of keys are split into: no part is short.
@@ -340,6 +343,11 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
   constexpr bool kFused = D < 256;
   const float scale = a.scale_log2;
   float ref = neg_inf(), sum = 0.0f;  // reference (log2 units) and this half's weights
+  // These, rounded as the second product takes them: summed by products of ones with 16 blocks of
+  // 4x4, in which every lane has a column of its own, so that a NaN stays with its query (the sum
+  // comes four times).  Against no second sum: 4593 rows of 128-wide heads 222 -> 229 us, two prompts
+  // of 2500 of 64-wide ones 69 -> 74; with dot products on the vector ALUs 231 and 74.
+  v4f rounded = {0.0f, 0.0f, 0.0f, 0.0f};
   float base = 0.0f;                  // weights of the current scores: exp2(s * scale - base)
 
   // S^T of a tile.
@@ -376,6 +384,7 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
       const float f = moves ? __builtin_amdgcn_exp2f(ref - top) : 1.0f;
       ref = moves ? top : ref;
       sum *= f;
+      rounded *= f;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -404,7 +413,11 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
       sum += x + y;
       w[e / 2] = cvt_bf16x2(x, y);
     }
-    return __builtin_bit_cast(v8bf, v4u{w[0], w[1], w[2], w[3]});
+    const v8bf p = __builtin_bit_cast(v8bf, v4u{w[0], w[1], w[2], w[3]});
+    const v4s ones = {0x3F80, 0x3F80, 0x3F80, 0x3F80};
+    rounded = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(ones, __builtin_bit_cast(v4s, v2u{w[0], w[1]}), rounded, 0, 0, 0);
+    rounded = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(ones, __builtin_bit_cast(v4s, v2u{w[2], w[3]}), rounded, 0, 0, 0);
+    return p;
   };
   // V^T of 16 keys (step st of the tile) and 32 values, in the order of the weights.
   auto v_frag = [&](const uint16_t* vt, int st, int i) {
@@ -540,7 +553,7 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
         }
     }
   }
-  const float total = sum_over_halves(sum);
+  const float total = sum_over_halves(sum), of_rounded = sum_over_halves(rounded[0]);
   if (parts > 1) {
     if (row >= lq) return;
     const int64_t at = (int64_t(index) * a.most_parts + part) * kPrefillRows + wave * kWaveRows + col;
@@ -550,7 +563,7 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
       for (int r = 0; r < 16; r += 4)
         *reinterpret_cast<float4*>(a.sums + at * D + 32 * i + 2 * r + 4 * half) =
             make_float4(o[i][r], o[i][r + 1], o[i][r + 2], o[i][r + 3]);
-    if (half == 0) a.stats[at] = make_float2(ref, total);
+    if (half == 0) a.stats[at] = make_float4(ref, total, of_rounded, 0.0f);
     return;
   }
   if (a.lse && half == 0 && row < lq)
@@ -559,7 +572,7 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
   // A lane holds every other four values of a row: through LDS, whole rows are stored at once (a
   // batch of eight prompts of up to 2048: 107 us, 112 with 8-byte stores to 32 rows each; alone, 37
   // queries: 6.3 us, not 6.1).  The keys' buffers are free: behind the last barrier no wave reads keys.
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  const float inv = total == 0.0f ? 0.0f : 1.0f / of_rounded;
   uint16_t* const rows = (wave < kWaves / 2 ? k0 : k1) + wave % (kWaves / 2) * kWaveRows * D;
   constexpr int kTurn = kChunks < 16 ? kChunks - 1 : 15;  // rows' chunks are turned by these bits
 #pragma unroll
@@ -598,22 +611,23 @@ __global__ __launch_bounds__(kPrefillJoinThreads) void prefill_join_kernel(const
   if (!find_item(a, index, &it)) return;
   const int parts = parts_of(a, it.key_tiles(a)), row = it.tile * kPrefillRows + r;
   if (parts > 1 && row < it.lq) {
-    float ref = neg_inf(), total = 0.0f;
+    float ref = neg_inf(), total = 0.0f, rounded = 0.0f;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
     for (int p = 0; p < parts; ++p) {
       const int64_t at = (int64_t(index) * a.most_parts + p) * kPrefillRows + r;
       const float4 x = *reinterpret_cast<const float4*>(a.sums + at * D + d);
-      const float2 st = a.stats[at];
+      const float4 st = a.stats[at];
       const float to = fmaxf(ref, st.x);
       const float f = ref == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(ref - to);
       const float h = st.x == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(st.x - to);
       ref = to;
       total = total * f + st.y * h;
+      rounded = rounded * f + st.z * h;
       v.x = v.x * f + x.x * h; v.y = v.y * f + x.y * h;
       v.z = v.z * f + x.z * h; v.w = v.w * f + x.w * h;
     }
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    const float inv = total == 0.0f ? 0.0f : 1.0f / rounded;
     *reinterpret_cast<uint2*>(a.out + int64_t(it.q0 + row) * a.os + int64_t(it.head) * D + d) =
         make_uint2(cvt_bf16x2(v.x * inv, v.y * inv), cvt_bf16x2(v.z * inv, v.w * inv));
     if (a.lse && d == 0)
@@ -660,7 +674,7 @@ PrefillPlan prefill_plan(int32_t seqs, int32_t total_q, int32_t total_k, int32_t
   if (p.parts == 1) return p;
   const uint64_t rows = uint64_t(p.items) * p.parts * kPrefillRows;
   p.sums_bytes = rows * d * 4;
-  p.bytes = p.sums_bytes + rows * 8;
+  p.bytes = p.sums_bytes + rows * 16;
   return p;
 }
 
@@ -724,7 +738,7 @@ extern "C" int attn_prefill(const uint16_t* q, const uint16_t* k, const uint16_t
   a.hkv = num_kv_heads, a.causal = causal != 0, a.scale_log2 = softmax_scale * kLog2e;
   a.most_parts = p.parts, a.items = int(p.items);
   a.sums = static_cast<float*>(workspace);
-  a.stats = p.bytes ? reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.sums_bytes) : nullptr;
+  a.stats = p.bytes ? reinterpret_cast<float4*>(static_cast<uint8_t*>(workspace) + p.sums_bytes) : nullptr;
   // parts of an item lie 8 workgroups apart: whole eights of items
   const int64_t blocks = p.parts == 1 ? p.items : (p.items + 7) / 8 * 8 * p.parts;
   const int64_t joins = p.items * (kPrefillRows / join_rows(head_dim));
