@@ -398,8 +398,9 @@ int fp8_qk_norm_rope_kv_write(const uint16_t* q, const uint16_t* k, const uint16
  *   out[i]  = bf16_rne( sum_j exp(s[i][j]) v[j] / sum_j exp(s[i][j]) )
  *   lse[i]  = log sum_j exp(s[i][j])
  * A query that sees no key gets zeros and lse = -infinity.  What a query does not see does not
- * reach it, infinities and NaN included.  FP32 products, sums and statistics; out's weights are
- * rounded to bf16, in its numerator and its denominator alike.
+ * reach it, infinities and NaN included.  An infinity or a NaN in a value row reaches the outputs of
+ * all queries that see it, however small its weight (infinities of both signs: NaN).  FP32 products,
+ * sums and statistics; out's weights are rounded to bf16, in its numerator and its denominator alike.
  *   q, k, v   device bf16 rows at q_stride / key_stride / value_stride elements, 16-byte aligned
  *   out       device bf16 rows at out_stride; rows outside every sequence are left untouched
  *   lse       device fp32 [total_q, num_q_heads], or NULL

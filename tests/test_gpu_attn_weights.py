@@ -48,3 +48,46 @@ def test_one_weight_above_all_others(d, lq, lk, at):
     attn_ref.check(out, w * top, bound, "out")
     want = torch.log1p(torch.exp(s))
     attn_ref.check(lse[:, 0], want, ((d + 8) * 6 + 64) * attn_ref.U24 + 0 * want, "lse")
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lq,lk,causal", [(300, 300, True), (40, 300, False), (20, 3000, False)])
+@pytest.mark.parametrize("at", [3, 130, -3])  # a tile that every query sees whole, one of few, the last
+def test_values_that_are_not_finite_reach_all_that_see_them(d, lq, lk, causal, at):
+    """Scores of 0 and +-200, so that most weights are 0 in binary32, before or behind the largest:
+    an infinity reaches every query that sees it, in its columns, wherever its key lies and however
+    the call is split; with one of the other sign beside it, or a NaN, the sum is NaN; a query with
+    a score that is NaN is NaN throughout.  Nothing else changes."""
+    g = torch.Generator(device=DEV).manual_seed(d + lq)
+    at %= lk
+    level = torch.randint(-1, 2, (lk, 1), generator=g, device=DEV) * 200.0
+    sign = torch.randint(0, 2, (lq, 1), generator=g, device=DEV) * 2.0 - 1
+    k, q = level.expand(lk, d).to(BF16).contiguous(), (sign / d).expand(lq, d).to(BF16).contiguous()
+    v = torch.randn((lk, d), generator=g, device=DEV).to(BF16)
+    sees = attn_ref.causal_mask(lq, lk, DEV) if causal else torch.ones((lq, lk), dtype=torch.bool, device=DEV)
+
+    def run(k, v):
+        return fq.attn_prefill(q, k, v, _cu(lq), 1, 1, d, cu_seqlens_k=_cu(lk), softmax_scale=1.0, causal=causal)
+
+    want = run(k, v)
+    assert torch.isfinite(want.float()).all()
+    assert (fq.attn_prefill_workspace_size(1, lq, lk, 1, 1, d) > 0) == (lk > 1000)
+    cols = torch.tensor([0, 5, 6, d - 1], device=DEV)
+    for bad in (math.inf, -math.inf, math.nan):
+        v2 = v.clone()
+        v2[at, cols] = bad
+        expect = want.clone()
+        expect[:, cols] = torch.where(sees[:, at, None], bad, want[:, cols].float()).to(BF16)
+        assert torch.equal(run(k, v2).nan_to_num(9e9, 8e9, 7e9), expect.nan_to_num(9e9, 8e9, 7e9)), bad
+    other = (at + 90) % lk
+    v2 = v.clone()
+    v2[at, cols], v2[other, cols] = math.inf, -math.inf
+    a, b = sees[:, at, None], sees[:, other, None]
+    expect = want.clone()
+    expect[:, cols] = torch.where(a & b, math.nan, torch.where(a, math.inf, torch.where(
+        b, -math.inf, want[:, cols].float()))).to(BF16)
+    assert torch.equal(run(k, v2).nan_to_num(9e9, 8e9, 7e9), expect.nan_to_num(9e9, 8e9, 7e9))
+    k2 = k.clone()
+    k2[other] = math.nan
+    expect = torch.where(b, math.nan, expect.float()).to(BF16)
+    assert torch.equal(run(k2, v2).nan_to_num(9e9, 8e9, 7e9), expect.nan_to_num(9e9, 8e9, 7e9))
