@@ -54,15 +54,20 @@ struct PrefillArgs {
   int items;         // work items there is room for
   int most_parts;    // parts of a tile's keys; 1: not split
   float scale_log2;  // softmax scale * log2(e)
-  float* sums;       // [work items][parts][rows][D] where split
-  float4* stats;     // [work items][parts][rows]: reference (log2 units), sums of the weights and
-                     // of the rounded ones, not 0: values were held to finite ones
+  float* sums;       // [parts][hq][tq][D] where split
+  float4* stats;     // [parts][hq][tq]: reference (log2 units), sums of the weights and of the
+                     // rounded ones, not 0: values were held to finite ones
 };
 
 // Parts that `tiles` tiles of keys are split into: no part is short.
 constexpr int kPartTiles = 4;
 __device__ __forceinline__ int parts_of(const PrefillArgs& a, int tiles) {
   return max(min(a.most_parts, tiles / kPartTiles), 1);
+}
+
+// The place of a query row's sums of one part and head.
+__device__ __forceinline__ int64_t sums_at(const PrefillArgs& a, int part, int head, int q_row) {
+  return (int64_t(part) * a.hq + head) * a.tq + q_row;
 }
 
 // Start and length of sequence s among `total` rows, whatever the list holds.
@@ -563,7 +568,7 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
   const float total = sum_over_halves(sum), of_rounded = sum_over_halves(rounded[0]);
   if (parts > 1) {
     if (row >= lq) return;
-    const int64_t at = (int64_t(index) * a.most_parts + part) * kPrefillRows + wave * kWaveRows + col;
+    const int64_t at = sums_at(a, part, head, q0 + row);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -650,7 +655,7 @@ __global__ __launch_bounds__(kPrefillJoinThreads) void prefill_join_kernel(const
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
     for (int p = 0; p < parts; ++p) {
-      const int64_t at = (int64_t(index) * a.most_parts + p) * kPrefillRows + r;
+      const int64_t at = sums_at(a, p, it.head, it.q0 + row);
       const float4 x = *reinterpret_cast<const float4*>(a.sums + at * D + d);
       const float4 st = a.stats[at];
       const float to = fmaxf(ref, st.x);
@@ -684,8 +689,12 @@ __global__ __launch_bounds__(kPrefillJoinThreads) void prefill_join_kernel(const
 // Work items of a call (an upper bound: tiles of whole sequences), and the parts that their keys
 // are split into: the number with the least estimated time.  A workgroup alone on its CU takes
 // about 1 us a tile of 64 keys (128-wide heads), two on one CU about 2; joining parts costs a
-// launch and the way of their sums through memory.  512 queries of 40 heads over 8704 keys: 144 us
-// in one part, 101 in three; 23 queries over 2794 keys, 10 heads: 44 us in one, 17 in eleven.
+// launch (4 us) and the way of their sums through memory, there and back at 5 TB/s.  As the lengths
+// are known only in the mean here, a split has to promise a fifth of the time.  512 queries of 40 heads
+// over 8704 keys: 144 us in one part, 105 in three; 23 queries over 2794 keys, 10 heads: 44 us in
+// one, 17 in eleven.  The sums take at most kMostSums: more parts than fit there were estimated to
+// gain 5 % in the mean and a third at most, on calls of milliseconds.
+constexpr uint64_t kMostSums = uint64_t(256) << 20;
 struct PrefillPlan {
   int64_t items;
   int parts;
@@ -703,10 +712,11 @@ PrefillPlan prefill_plan(int32_t seqs, int32_t total_q, int32_t total_k, int32_t
   // under a causal mask prompts without a history see half of their keys in the mean
   const bool history = total_k > 2 * int64_t(total_q);
   const double spread = double(p.items) * mean * (history ? 1.0 : 0.5) / cus * tile_us;
+  const uint64_t part_rows = uint64_t(total_q) * hq, part_bytes = part_rows * (d * 4 + 16);
   double best = 0.0;
   for (int n = 1; n <= 64 && n * kPartTiles <= longest + 1; ++n) {
     const int64_t groups = p.items * n;
-    if (n > 1 && !history && groups > cus) break;
+    if (n > 1 && (n * part_bytes > kMostSums || (!history && groups > cus))) break;
     const int64_t rounds = groups <= cus ? 1 : 2 * ((groups + 2 * cus - 1) / (2 * cus));
     const double path = longest / n * tile_us * rounds;
     double us = path > spread ? path : spread;
@@ -717,9 +727,8 @@ PrefillPlan prefill_plan(int32_t seqs, int32_t total_q, int32_t total_k, int32_t
     }
   }
   if (p.parts == 1) return p;
-  const uint64_t rows = uint64_t(p.items) * p.parts * kPrefillRows;
-  p.sums_bytes = rows * d * 4;
-  p.bytes = p.sums_bytes + rows * 16;
+  p.sums_bytes = p.parts * part_rows * d * 4;
+  p.bytes = p.parts * part_bytes;
   return p;
 }
 

@@ -410,7 +410,8 @@ int fp8_qk_norm_rope_kv_write(const uint16_t* q, const uint16_t* k, const uint16
  *   at most 2^23; total_q, total_k <= 2^30; 0 < softmax_scale <= 2^64.
  *   workspace   device memory of workspace_bytes >= attn_prefill_workspace_size's, 256-byte
  *               aligned, of any content (nothing is kept in it from call to call); calls that
- *               share one must not overlap in time; NULL is fine where the size is 0
+ *               share one must not overlap in time; NULL is fine where the size is 0.  At most
+ *               256 MiB: a few binary32 rows for each query row and head
  * Few queries over long keys are split along the keys: then two kernels are enqueued, the second
  * joining the parts in order, and a workspace is needed (results do not depend on the order in
  * which workgroups run).  attn_prefill_workspace_size: for the current device.
