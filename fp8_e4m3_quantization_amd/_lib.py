@@ -721,9 +721,13 @@ def _check_lse(lse, rows, heads):
 _ATTN_SIZES = {}       # (entry point, device index, shape) -> its workspace size there
 
 
+_KEPT_WORKSPACES, _KEPT_BYTES = 8, 64 << 20
+
+
 class _Workspaces(threading.local):
     """(device index, stream) -> uint8 tensor; each thread has its own, since the two kernels of one
-    call may be enqueued around those of another thread's call on the same stream."""
+    call may be enqueued around those of another thread's call on the same stream.  At most
+    _KEPT_WORKSPACES of at most _KEPT_BYTES each."""
 
     def __init__(self):
         self.of = {}
@@ -740,8 +744,10 @@ def _workspace_size(fn: str, *shape) -> int:
 
 def _attn_workspace(fn: str, index: int, stream, *shape):
     """A workspace for a call of this shape on `stream` of GPU `index`, kept and reused by later
-    calls of this thread there; None where none is needed.  While a graph is being captured a new
-    one is made instead, in the graph's own memory, so that no two graphs share one."""
+    calls of this thread there; None where none is needed.  Large ones are made for the call, and
+    while a graph is being captured a new one is, in the graph's own memory, so that no two graphs
+    share one.  One that is let go stays the stream's own until what is enqueued there has used it:
+    the allocator gives its memory to later work of the same stream only."""
     need = _ATTN_SIZES.get((fn, index, shape))
     if need == 0:
         return None
@@ -756,13 +762,17 @@ def _attn_workspace(fn: str, index: int, stream, *shape):
     if stream is not None and stream != torch._C._cuda_getCurrentRawStream(index):
         with _on_stream(stream, torch.device("cuda", index)):
             return _attn_workspace(fn, index, None, *shape)
-    if torch._C._cuda_isCurrentStreamCapturing():
+    if need > _KEPT_BYTES or torch._C._cuda_isCurrentStreamCapturing():
         return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
     key = (index, torch._C._cuda_getCurrentRawStream(index))
-    ws = _ATTN_WORKSPACES.of.get(key)
+    kept = _ATTN_WORKSPACES.of
+    ws = kept.get(key)
     if ws is None or ws.numel() < need:
-        ws = _ATTN_WORKSPACES.of[key] = torch.empty(need, dtype=torch.uint8,
-                                                    device=torch.device("cuda", index))
+        ws = None
+        kept.pop(key, None)
+        while len(kept) >= _KEPT_WORKSPACES:
+            del kept[next(iter(kept))]
+        ws = kept[key] = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
     return ws
 
 
