@@ -627,6 +627,8 @@ def _on_stream(stream, device):
     """Allocations and fills inside go to `stream` (the current one when None)."""
     if stream is None:
         return contextlib.nullcontext()
+    if stream == 0:  # ExternalStream takes this for "no handle" and makes a stream of its own
+        return torch.cuda.stream(torch.cuda.default_stream(device))
     return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device))
 
 
