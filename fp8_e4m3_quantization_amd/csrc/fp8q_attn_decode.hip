@@ -461,7 +461,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const DecodeArgs a, 
 }
 
 int decode_shape(int32_t seqs, int32_t hq, int32_t hkv, int32_t d) {
-  if (seqs < 0 || seqs > (1 << 20) || hq <= 0 || hkv <= 0 || hq % hkv != 0 || hq > 65536)
+  if (seqs < 0 || seqs > kMostSeqs || hq <= 0 || hkv <= 0 || hq % hkv != 0 || hq > 65536)
     return FP8Q_EINVAL;
   if (d != 64 && d != 128 && d != 256) return FP8Q_EINVAL;
   return FP8Q_OK;

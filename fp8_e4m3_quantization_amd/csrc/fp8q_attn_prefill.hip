@@ -734,7 +734,7 @@ PrefillPlan prefill_plan(int32_t seqs, int32_t total_q, int32_t total_k, int32_t
 
 int prefill_shape(int32_t seqs, int32_t total_q, int32_t total_k, int32_t hq, int32_t hkv, int32_t d) {
   if (seqs < 0 || total_q < 0 || total_k < 0 || total_q > (1 << 30) || total_k > (1 << 30) ||
-      seqs > (1 << 24))
+      seqs > kMostSeqs)
     return FP8Q_EINVAL;
   if (hq <= 0 || hkv <= 0 || hq % hkv != 0 || hq > 65536) return FP8Q_EINVAL;
   if (d != 64 && d != 128 && d != 256) return FP8Q_EINVAL;

@@ -407,7 +407,7 @@ int fp8_qk_norm_rope_kv_write(const uint16_t* q, const uint16_t* k, const uint16
  *   cu_seqlens_q, cu_seqlens_k  device int32 [num_seqs + 1], ascending from 0 to at most total_q /
  *             total_k (the rows of q and of k); entries are clamped to that range
  *   head_dim in {64, 128, 256}; num_q_heads a multiple of num_kv_heads; strides multiples of 8,
- *   at most 2^23; total_q, total_k <= 2^30; 0 < softmax_scale <= 2^64.
+ *   at most 2^23; num_seqs <= 65536; total_q, total_k <= 2^30; 0 < softmax_scale <= 2^64.
  *   workspace   device memory of workspace_bytes >= attn_prefill_workspace_size's, 256-byte
  *               aligned, of any content (nothing is kept in it from call to call); calls that
  *               share one must not overlap in time; NULL is fine where the size is 0.  At most
@@ -450,7 +450,7 @@ int attn_prefill(const uint16_t* q, const uint16_t* k, const uint16_t* v,
  *               aligned, of any content (nothing is kept in it from call to call); calls that
  *               share one must not overlap in time
  *   head_dim in {64, 128, 256}; num_q_heads a multiple of num_kv_heads; block_size > 0;
- *   max_blocks * block_size <= 2^30 and num_seqs * (max_blocks * block_size / 32 + 1) <= 2^30;
+ *   num_seqs <= 65536; max_blocks * block_size <= 2^30 and num_seqs * (max_blocks * block_size / 32 + 1) <= 2^30;
  *   cache_stride >= block_size*H*D, a multiple of 16; q / out
  *   strides multiples of 8; k_scale, v_scale in [2^-64, 2^64]; 0 < softmax_scale <= 2^32.
  * The scores must stay within binary32.  Outputs must not overlap inputs.

@@ -52,3 +52,15 @@ def test_the_binding_keeps_few_workspaces():
     a, b = (fq.attn_prefill(q, k, v, cu_q, hq, 4, d, cu_seqlens_k=cu_k) for _ in range(2))
     assert torch.equal(a, b)
     assert all(t.numel() <= 64 << 20 for t in _lib._ATTN_WORKSPACES.of.values())
+
+
+def test_calls_of_too_many_sequences_are_refused():
+    """Every workgroup searches all lengths: beyond 65536 sequences a call would run for seconds to
+    minutes.  (Nothing is enqueued: the checks return before any pointer is looked at.)"""
+    assert fq.fp8_attn_decode_workspace_size(1 << 16, 8, 2, 128) > 0
+    assert fq.attn_prefill_workspace_size(1 << 16, 1 << 16, 1 << 16, 8, 2, 128) == 0
+    n = (1 << 16) + 1
+    for call in (lambda: fq.fp8_attn_decode_workspace_size(n, 8, 2, 128),
+                 lambda: fq.attn_prefill_workspace_size(n, n, n, 8, 2, 128)):
+        with pytest.raises(_lib.Fp8qError, match="-1"):
+            call()
