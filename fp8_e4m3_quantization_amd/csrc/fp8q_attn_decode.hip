@@ -12,16 +12,17 @@
 // straight to registers.  A lane of row group g (lanes 16 g ..) ends with the scores of positions
 // 4g..4g+3 and 16+4g..16+4g+3 of the tile, which are taken as its 8 of the 32 summed by the
 // second product as they lie; it loads V at the same 8 positions, bytes D/16 (l % 16) onwards,
-// so that both operands agree without an exchange.  P is rounded to bf16 for that product (at
-// most 2^-9 of each weight, under the output's own rounding); out's denominator is the sum of the
-// rounded weights (one more row of the product, of ones), so that a weight that outweighs all
+// so that both operands agree without an exchange.  P is rounded to bf16 for that product (by
+// up to 2^-8 of each weight, as much as the output's own rounding); out's denominator is the sum of
+// the rounded weights (one more row of the product, of ones), so that a weight that outweighs all
 // others loses nothing by its rounding; lse is of the unrounded ones.
 //
 // The histories of all sequences, laid end to end, are cut into equal shares, one for each CU,
 // whatever the lengths.  A workgroup's waves take the KV heads of its share side by side (a
 // token's heads lie side by side in the pools) and, with fewer heads than waves, its tiles in
 // turn.  A sequence that lies in several shares leaves their sums in the workspace, and a second
-// kernel adds them in the sequence's order: results do not depend on the order of workgroups.
+// kernel adds them in the sequence's order: results do not depend on the order of workgroups.  Where
+// the table has room for kWholeMost positions at most, every sequence is a share of its own.
 // One workgroup a CU: more read no faster.  Measured: 64 sequences of 500 to 8100 positions, 8 KV
 // heads of 128 (525 MB): 95 us and 6 for the join, 5.5 TB/s; 2 of 131072 and 100003, 4 KV heads:
 // 46 us and 7, 5.2 TB/s (a plain read stream: 5.9-6.2).
@@ -41,7 +42,11 @@ namespace {
 constexpr int kDecTile = 32;                        // positions a wave takes at a time
 constexpr int kDecRows = 16;                        // query heads of a workgroup
 constexpr int kDecPerCu = 1;                        // workgroups on a CU at once
-constexpr int kWholeMost = 1024;                    // histories up to this long are not cut
+// No history is cut where the table has room for at most this many positions a sequence (the host
+// does not know the lengths).  The same histories behind a wider table take the second kernel too: one
+// of 777 positions, 40 heads: 10.5 us with a table of 784, 12.1 with one of 32768; 128 of 300, 32
+// heads, 8 KV heads: 17.1 and 26.2.
+constexpr int kWholeMost = 1024;
 constexpr int kJoinAtOnce = 8;                      // parts whose sums a thread has in flight
 
 struct DecodeArgs {
@@ -480,7 +485,7 @@ DecodePlan decode_plan(int32_t hq, int32_t hkv, int32_t d, int32_t seqs, int64_t
   p.heads = hkv * p.row_tiles;
   p.rows = group < kDecRows ? group : kDecRows;
   p.together = 1;
-  // Short histories: a sequence is a share, with no second kernel, and one head for all the
+  // Tables of short histories: a sequence is a share, with no second kernel, and one head for all the
   // waves of a workgroup as long as that leaves no CU with two.
   if (most <= kWholeMost) {
     while (p.together < waves_of(d) && p.heads % (2 * p.together) == 0 &&

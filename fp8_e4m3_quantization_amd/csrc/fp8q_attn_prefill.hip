@@ -19,11 +19,13 @@
 //
 // Bound: matrix cores and vector ALUs alike (a score costs as long in its exponential as in its
 // products at 128-wide heads), two waves of a SIMD overlapping them: 4593 queries of 40 heads,
-// 4 KV heads, 128 wide, causal (217 GFLOP) take 217 us, 1.0 PFLOP/s, at a clock of 1.85 GHz under
-// that load; matrix cores are busy 56 % and vector ALUs 51 % of the time, LDS 29 %.  The products
-// and copies alone take 166 us, with the softmax 190.  128 queries a workgroup: 32 a wave, since o,
-// two tiles of scores and q fill the registers of two waves a SIMD (64 a wave, alone on its SIMD:
-// 320 us).  64-wide heads: three waves a SIMD, two prompts of 2500 in 67 us, vector ALUs busy 72 %.
+// 4 KV heads, 128 wide, causal (217 GFLOP) take 227 us, 0.95 PFLOP/s, call after call (the first
+// dozens of calls up to 275: the clock falls to 1.75 GHz under that load before it settles); matrix
+// cores are busy 57 % and vector ALUs 51 % of the time, LDS 28 %.  Without the sum of the rounded
+// weights it is 7 us less; of those 217, the products and copies alone take 166, with the softmax 190.
+// 128 queries a workgroup: 32 a wave, since o, two tiles of scores and q fill the registers of two
+// waves a SIMD (64 a wave, alone on its SIMD: 320 us).  64-wide heads: three waves a SIMD, two prompts
+// of 2500 in 74 us, vector ALUs busy 70 %, matrix cores 43 %.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>

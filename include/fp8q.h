@@ -415,7 +415,8 @@ int fp8_qk_norm_rope_kv_write(const uint16_t* q, const uint16_t* k, const uint16
  * Few queries over long keys are split along the keys: then two kernels are enqueued, the second
  * joining the parts in order, and a workspace is needed (results do not depend on the order in
  * which workgroups run).  attn_prefill_workspace_size: for the current device.
- * The scores must stay within binary32.  Outputs must not overlap inputs.
+ * The scores, and 2^8 times a row's sum of |v|, must stay within binary32.  Outputs must not
+ * overlap inputs.
  * Errors: FP8Q_EINVAL, FP8Q_ENULL, FP8Q_EALIGN, FP8Q_ELAUNCH. */
 int attn_prefill_workspace_size(int32_t num_seqs, int32_t total_q, int32_t total_k,
                                 int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
@@ -439,9 +440,9 @@ int attn_prefill(const uint16_t* q, const uint16_t* k, const uint16_t* v,
  *   lse[s][h] = log sum_p exp(s[p])
  * len is clamped to [0, max_blocks * block_size]; positions in a block outside [0, num_blocks)
  * do not count; a sequence without positions gets zeros and lse = -infinity.  FP32 products,
- * sums and statistics; the weights are rounded to bf16 for their product with V.  What lies in
- * the pools behind a sequence's end does not reach it, NaN codes included.  Results do not
- * depend on the order in which workgroups run.
+ * sums and statistics; out's weights are rounded to bf16, in its numerator and its denominator
+ * alike.  What lies in the pools behind a sequence's end does not reach it, NaN codes included.
+ * Results do not depend on the order in which workgroups run.
  *   q, out      device bf16 rows at q_stride / out_stride elements, 16-byte aligned
  *   k_cache, v_cache  device uint8 pools of num_blocks * cache_stride bytes, 16-byte aligned
  *   block_tables      device int32 [num_seqs, table_stride], the first max_blocks of each row used
@@ -454,8 +455,9 @@ int attn_prefill(const uint16_t* q, const uint16_t* k, const uint16_t* v,
  *   cache_stride >= block_size*H*D, a multiple of 16; q / out
  *   strides multiples of 8; k_scale, v_scale in [2^-64, 2^64]; 0 < softmax_scale <= 2^32.
  * The scores must stay within binary32.  Outputs must not overlap inputs.
- * Enqueues two kernels where max_blocks * block_size > 1024 (the second joins the parts of
- * histories that were cut), else one.
+ * Enqueues two kernels where max_blocks * block_size > 1024, whatever the lengths (the second joins
+ * the parts of histories that were cut), else one: a table no wider than the longest history needs
+ * is the faster one for short histories.
  * fp8_attn_decode_workspace_size: for the current device.
  * Errors: FP8Q_EINVAL, FP8Q_ENULL, FP8Q_EALIGN, FP8Q_ELAUNCH. */
 int fp8_attn_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
