@@ -58,7 +58,7 @@ struct PrefillArgs {
   float scale_log2;  // softmax scale * log2(e)
   float* sums;       // [parts][hq][tq][D] where split
   float4* stats;     // [parts][hq][tq]: reference (log2 units), sums of the weights and of the
-                     // rounded ones, not 0: values were held to finite ones
+                     // rounded ones
 };
 
 // Parts that `tiles` tiles of keys are split into: no part is short.
@@ -224,23 +224,6 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w) {
   const v2us below = __builtin_elementwise_min(__builtin_bit_cast(v2us, w), v2us{0xFF7F, 0xFF7F});
   const v2s x = __builtin_elementwise_min(__builtin_bit_cast(v2s, below), v2s{0x7F7F, 0x7F7F});
   return __builtin_bit_cast(uint32_t, x);
-}
-
-// Sums of the infinities and NaNs in N neighbouring values (from p on, in rows `stride` apart) of keys
-// from .. to - 1; 0 where all are finite.
-template <int N>
-__device__ __forceinline__ void sum_not_finite(const uint16_t* p, int64_t stride, int from, int to, float* bad) {
-#pragma unroll
-  for (int e = 0; e < N; ++e) bad[e] = 0.0f;
-  for (int j = from; j < to; ++j) {
-    uint32_t w[N / 2];
-    __builtin_memcpy(w, __builtin_assume_aligned(p + j * stride, 2 * N), 2 * N);
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const float f = e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
-      bad[e] += __builtin_isfinite(f) ? 0.0f : f;
-    }
-  }
 }
 
 // The order of a turn of the pipeline below: the score products with the previous tile's weights
@@ -562,12 +545,60 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
     for (; t < tiles; ++t) next_tile(t & 1 ? k1 : k0, t & 1 ? v0 : v1);
   }
 
+  const float total = sum_over_halves(sum), of_rounded = sum_over_halves(rounded[0]);
   // An infinity or a NaN of a value that a query sees reaches its output however small its weight.  In
   // the tiles seen whole it left the sum infinite or NaN (a weight of 0 makes an infinity NaN), in the
-  // last ones it was held to a finite value: either way the output is made from the values
-  // themselves (rare).
-  const bool held = __any(odd != 0);
-  const float total = sum_over_halves(sum), of_rounded = sum_over_halves(rounded[0]);
+  // last ones it was held to a finite value: where there was any, the wave looks through its keys once
+  // more, 32 columns at a time, and such values' own sum takes the output's place (rare: one infinity
+  // early in 16384 tokens of 40 heads, 8.1 ms instead of 2.9; with a walk for each output 118).
+  float most = 0.0f;  // NaN where one is (compared as an integer: the compiler takes this for a number)
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) most = __builtin_elementwise_maximum(most, __builtin_fabsf(o[i][r]));
+  const bool fine = __all((__float_as_uint(most) & 0x7FFFFFFFu) < 0x7F800000u);
+  if (!fine || __any(odd != 0)) {
+    const int upto = min(my_tiles * kTileKeys, lk), sees = total == total ? limit : 0;  // (else all NaN)
+    const uint16_t* const base = a.v + int64_t(kv0) * a.vs + int64_t(kvh) * D;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      v16f bad;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) bad[r] = 0.0f;
+      for (int j0 = fine ? first_held : 0; j0 < upto; j0 += 64) {  // a lane reads 8 values of 4 keys
+        uint4 x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          x[u] = *reinterpret_cast<const uint4*>(base + min(j0 + 16 * u + (lane >> 2), upto - 1) * a.vs + 32 * i + 8 * (lane & 3));
+        bool found = false;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          auto finite = [](uint32_t w) { return w == finite2(w); };
+          uint64_t where = __ballot(!(finite(x[u].x) && finite(x[u].y) && finite(x[u].z) && finite(x[u].w)));
+          while (where) {
+            const int at = __builtin_ctzll(where) >> 2, j = j0 + 16 * u + at;
+            where &= ~(uint64_t(15) << (4 * at));
+            found = true;
+            const uint16_t* src = base + min(j, upto - 1) * a.vs + 32 * i + 4 * half;
+#pragma unroll
+            for (int r = 0; r < 16; r += 4) {
+              const uint2 y = *reinterpret_cast<const uint2*>(src + 2 * r);
+              const float f[4] = {bf16_lo(y.x), bf16_hi(y.x), bf16_lo(y.y), bf16_hi(y.y)};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) bad[r + e] += j >= sees || __builtin_isfinite(f[e]) ? 0.0f : f[e];
+            }
+          }
+        }
+        if (!found) continue;
+        bool done = true;  // what is NaN stays so
+#pragma unroll
+        for (int r = 0; r < 16; ++r) done &= bad[r] != bad[r];
+        if (__all(done || sees <= j0 + 64)) break;
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[i][r] = bad[r] == 0.0f ? o[i][r] : bad[r];
+    }
+  }
   if (parts > 1) {
     if (row >= lq) return;
     const int64_t at = sums_at(a, part, head, q0 + row);
@@ -577,7 +608,7 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
       for (int r = 0; r < 16; r += 4)
         *reinterpret_cast<float4*>(a.sums + at * D + 32 * i + 2 * r + 4 * half) =
             make_float4(o[i][r], o[i][r + 1], o[i][r + 2], o[i][r + 3]);
-    if (half == 0) a.stats[at] = make_float4(ref, total, of_rounded, held ? 1.0f : 0.0f);
+    if (half == 0) a.stats[at] = make_float4(ref, total, of_rounded, 0.0f);
     return;
   }
   if (a.lse && half == 0 && row < lq)
@@ -598,40 +629,12 @@ __device__ __forceinline__ void prefill_tile(const PrefillArgs& a) {
                      cvt_bf16x2(o[i][r + 2] * inv, o[i][r + 3] * inv));
   asm volatile("" ::: "memory");  // the wave's own writes, read by other lanes below
   __builtin_amdgcn_wave_barrier();
-  auto staged = [&](int r, int c) { return *reinterpret_cast<const uint4*>(rows + r * D + (c ^ (r & kTurn)) * 8); };
-  auto finite = [&](uint4 x) {
-    return x.x == finite2(x.x) && x.y == finite2(x.y) && x.z == finite2(x.z) && x.w == finite2(x.w);
-  };
-  auto at = [&](int r, int c) {
-    return reinterpret_cast<uint4*>(a.out + int64_t(q0 + mine + r) * a.os + int64_t(head) * D + 8 * c);
-  };
 #pragma unroll
   for (int j = 0; j < kWaveRows * kChunks / 64; ++j) {
     const int r = (64 * j + lane) / kChunks, c = lane % kChunks;
-    const uint4 x = staged(r, c);
-    if (mine + r < lq) *at(r, c) = x;
-  }
-  float most = 0.0f;  // NaN where one is (compared as an integer: the compiler takes this for a number)
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) most = __builtin_elementwise_maximum(most, __builtin_fabsf(o[i][r]));
-  if (!held && __all((__float_as_uint(most) & 0x7FFFFFFFu) < 0x7F800000u)) return;
-  const uint64_t nan_rows = __ballot(total != total);  // scores that are NaN: rows of NaN, as they are
-#pragma unroll 1
-  for (int j = 0; j < kWaveRows * kChunks / 64; ++j) {
-    const int r = (64 * j + lane) / kChunks, c = lane % kChunks;
-    const uint4 x = staged(r, c);
-    const bool fine = finite(x);
-    if (mine + r >= lq || (nan_rows >> r & 1) || (fine && !held)) continue;
-    float bad[8];
-    sum_not_finite<8>(a.v + int64_t(kv0) * a.vs + int64_t(kvh) * D + 8 * c, a.vs, fine ? first_held : 0,
-                      seen(mine + r), bad);
-    auto settled = [&](uint32_t w, int e) {
-      return (bad[e] == 0.0f ? w & 0xFFFFu : f32_to_bf16_bits(bad[e])) |
-             (bad[e + 1] == 0.0f ? w & 0xFFFF0000u : f32_to_bf16_bits(bad[e + 1]) << 16);
-    };
-    *at(r, c) = make_uint4(settled(x.x, 0), settled(x.y, 2), settled(x.z, 4), settled(x.w, 6));
+    const uint4 x = *reinterpret_cast<const uint4*>(rows + r * D + (c ^ (r & kTurn)) * 8);
+    if (mine + r < lq)
+      *reinterpret_cast<uint4*>(a.out + int64_t(q0 + mine + r) * a.os + int64_t(head) * D + 8 * c) = x;
   }
 }
 
@@ -653,7 +656,7 @@ __global__ __launch_bounds__(kPrefillJoinThreads) void prefill_join_kernel(const
   if (!find_item(a, index, &it)) return;
   const int parts = parts_of(a, it.key_tiles(a)), row = it.tile * kPrefillRows + r;
   if (parts > 1 && row < it.lq) {
-    float ref = neg_inf(), total = 0.0f, rounded = 0.0f, held = 0.0f;
+    float ref = neg_inf(), total = 0.0f, rounded = 0.0f;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
     for (int p = 0; p < parts; ++p) {
@@ -666,22 +669,24 @@ __global__ __launch_bounds__(kPrefillJoinThreads) void prefill_join_kernel(const
       ref = to;
       total = total * f + st.y * h;
       rounded = rounded * f + st.z * h;
-      held += st.w;
       v.x = v.x * f + x.x * h; v.y = v.y * f + x.y * h;
       v.z = v.z * f + x.z * h; v.w = v.w * f + x.w * h;
     }
     const float inv = total == 0.0f ? 0.0f : 1.0f / rounded;
-    if ((held != 0.0f || !__builtin_isfinite(v.x + v.y + v.z + v.w)) && total == total) {
-      float bad[4];
-      sum_not_finite<4>(a.v + int64_t(it.kv0) * a.vs + int64_t(it.head / (a.hq / a.hkv)) * D + d, a.vs, 0,
-                        it.seen(a, row), bad);
-      v.x = bad[0] == 0.0f ? v.x : bad[0];
-      v.y = bad[1] == 0.0f ? v.y : bad[1];
-      v.z = bad[2] == 0.0f ? v.z : bad[2];
-      v.w = bad[3] == 0.0f ? v.w : bad[3];
+    float y[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+    // a part that is infinite or NaN counts whatever its weight, which may be 0 (rare)
+    if (!__builtin_isfinite(v.x + v.y + v.z + v.w)) {
+      float bad[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int p = 0; p < parts; ++p) {
+        const float* x = a.sums + sums_at(a, p, it.head, it.q0 + row) * D + d;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bad[e] += __builtin_isfinite(x[e]) ? 0.0f : x[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = bad[e] == 0.0f ? y[e] : bad[e];
     }
     *reinterpret_cast<uint2*>(a.out + int64_t(it.q0 + row) * a.os + int64_t(it.head) * D + d) =
-        make_uint2(cvt_bf16x2(v.x * inv, v.y * inv), cvt_bf16x2(v.z * inv, v.w * inv));
+        make_uint2(cvt_bf16x2(y[0], y[1]), cvt_bf16x2(y[2], y[3]));
     if (a.lse && d == 0)
       a.lse[int64_t(it.q0 + row) * a.hq + it.head] =
           total == 0.0f ? neg_inf() : (ref + __builtin_amdgcn_logf(total)) * kLn2;

@@ -91,3 +91,24 @@ def test_values_that_are_not_finite_reach_all_that_see_them(d, lq, lk, causal, a
     k2[other] = math.nan
     expect = torch.where(b, math.nan, expect.float()).to(BF16)
     assert torch.equal(run(k2, v2).nan_to_num(9e9, 8e9, 7e9), expect.nan_to_num(9e9, 8e9, 7e9))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lq,lk,causal", [(300, 300, True), (33, 700, False), (20, 3000, False)])
+@pytest.mark.parametrize("kinds,share", [((math.inf, -math.inf, math.nan), 0.002), ((math.inf,), 0.3),
+                                         ((math.nan,), 1.0), ((math.inf, -math.inf), 0.6)])
+def test_many_values_that_are_not_finite(d, lq, lk, causal, kinds, share):
+    """What a query sees of a column decides: nothing but finite values, and the output is as if the
+    others were finite too; else the sum of those that are not."""
+    g = torch.Generator(device=DEV).manual_seed(d + lk)
+    q, k, v = (torch.randn((n, d), generator=g, device=DEV).to(BF16) * std
+               for n, std in ((lq, 30.0), (lk, 1.0), (lk, 1.0)))
+    kind = torch.tensor(kinds, device=DEV).to(BF16)[torch.randint(0, len(kinds), (lk, d), generator=g, device=DEV)]
+    hit = torch.rand((lk, d), generator=g, device=DEV) < share
+    v2 = torch.where(hit, kind, v)
+    sees = (attn_ref.causal_mask(lq, lk, DEV) if causal else torch.ones((lq, lk), dtype=torch.bool, device=DEV)).float()
+    up, down, nan = (sees @ x.float() > 0 for x in (v2 == math.inf, v2 == -math.inf, torch.isnan(v2)))
+    out = [fq.attn_prefill(q, k, x, _cu(lq), 1, 1, d, cu_seqlens_k=_cu(lk), causal=causal) for x in (v, v2)]
+    expect = torch.where(nan | (up & down), math.nan, torch.where(up, math.inf, torch.where(
+        down, -math.inf, out[0].float()))).to(BF16)
+    assert torch.equal(out[1].nan_to_num(9e9, 8e9, 7e9), expect.nan_to_num(9e9, 8e9, 7e9))
