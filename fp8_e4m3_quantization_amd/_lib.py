@@ -31,7 +31,8 @@ EXPORTS = (
     "fp8_kv_write", "fp8_kv_write_amax", "fp8_kv_read", "fp8_kv_amax",
     "qk_norm_rope", "fp8_qk_norm_rope_kv_write", "attn_prefill",
     "attn_prefill_workspace_size", "fp8_attn_decode_workspace_size", "fp8_attn_decode",
-    "fp8q_kv_calib_create", "fp8q_kv_calib_create_with_ops", "fp8q_kv_calib_observe",
+    "fp8_attn_chunk_workspace_size", "fp8_attn_chunk", "fp8_rms_norm_group_quant",
+    "fp8_silu_mul_group_quant", "fp8q_kv_calib_create", "fp8q_kv_calib_create_with_ops", "fp8q_kv_calib_observe",
     "fp8q_kv_calib_decide", "fp8q_kv_calib_scales", "fp8q_kv_calib_state",
     "fp8q_kv_calib_destroy",
 )
@@ -150,6 +151,14 @@ def load() -> ctypes.CDLL:
         "fp8_attn_decode": (ctypes.c_int, [P, P, P, P, P, P, P, I32, I32, I64, I32, I32, I32, I32,
                                            I64, F32, F32, F32, I64, I64, I64, P, ctypes.c_uint64,
                                            P]),
+        "fp8_attn_chunk_workspace_size": (ctypes.c_int, [I32, I32, I32, I32, I32,
+                                                         ctypes.POINTER(ctypes.c_uint64)]),
+        "fp8_attn_chunk": (ctypes.c_int, [P, P, P, P, P, P, P, P, I32, I32, I32, I64, I32, I32, I32,
+                                          I32, I64, F32, F32, F32, I32, I64, I64, I64, P,
+                                          ctypes.c_uint64, P]),
+        "fp8_rms_norm_group_quant": (ctypes.c_int, [P, P, P, F32, P, P, P, P, I64, I32, I64, I64,
+                                                    I64, I64, P]),
+        "fp8_silu_mul_group_quant": (ctypes.c_int, [P, P, P, P, P, I64, I32, I64, I64, I64, P]),
         "fp8q_kv_calib_create": (ctypes.c_int, [I32, F32, F32, ctypes.POINTER(P)]),
         "fp8q_kv_calib_create_with_ops": (ctypes.c_int, [I32, F32, F32,
                                                          ctypes.POINTER(KvCalibOps),
@@ -877,6 +886,142 @@ def fp8_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
           head_dim ** -0.5 if softmax_scale is None else softmax_scale, qs, os_, cs,
           _ptr(workspace, "workspace", _BYTES, i), workspace.numel())
     return out
+
+
+def fp8_attn_chunk_workspace_size(num_seqs: int, total_q: int, num_q_heads: int,
+                                  num_kv_heads: int, head_dim: int) -> int:
+    """Bytes of workspace that fp8_attn_chunk needs for this shape on the current device (0: none)."""
+    return _workspace_size("fp8_attn_chunk_workspace_size", num_seqs, total_q, num_q_heads,
+                           num_kv_heads, head_dim)
+
+
+def fp8_attn_chunk(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   block_tables: torch.Tensor, context_lens: torch.Tensor,
+                   cu_seqlens_q: torch.Tensor, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                   block_size: int, k_scale: float, v_scale: float,
+                   softmax_scale: float | None = None, causal: bool = True,
+                   out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                   cache_stride: int | None = None, workspace: torch.Tensor | None = None,
+                   stream: int | None = None) -> torch.Tensor:
+    """Attention of chunks of new tokens over the paged E4M3 cache: q [tokens, Hq * D] bf16, int32
+    cu_seqlens_q [num_seqs + 1], block_tables [num_seqs, max_blocks] and context_lens [num_seqs] (the
+    new tokens' positions included, the last ones, written before).  softmax_scale: head_dim ** -0.5
+    when None.  Rows outside every sequence are left as they were (zeros when allocated here); lse,
+    if given, is fp32 [tokens, Hq].  workspace: uint8, fp8_attn_chunk_workspace_size's bytes, for
+    one call at a time; by default one kept per thread and stream."""
+    tq, qs = _head_rows(q, "q", num_q_heads, head_dim)
+    cs = block_size * num_kv_heads * head_dim if cache_stride is None else cache_stride
+    blocks = _kv_num_blocks(k_cache, v_cache, cs)
+    n = context_lens.numel()
+    if len(block_tables.shape) != 2 or block_tables.shape[0] != n or cu_seqlens_q.numel() != n + 1:
+        raise ValueError("block_tables must be [num_seqs, max_blocks], context_lens [num_seqs], "
+                         "cu_seqlens_q [num_seqs + 1]")
+    width = block_tables.shape[1]
+    table_stride, inner = block_tables.stride()
+    if inner != 1 and width > 1:
+        raise ValueError("block_tables' rows must be packed")
+    if out is None:
+        with _on_stream(stream, q.device):
+            out = torch.zeros((tq, num_q_heads * head_dim), dtype=torch.bfloat16, device=q.device)
+    _, os_ = _head_rows(out, "out", num_q_heads, head_dim, tq)
+    _check_lse(lse, tq, num_q_heads)
+    i = _gpu_index(q, "q")
+    if n == 0 or tq == 0:
+        return out
+    if workspace is None:
+        workspace = _attn_workspace("fp8_attn_chunk_workspace_size", i, stream, n, tq, num_q_heads,
+                                    num_kv_heads, head_dim)
+    _call("fp8_attn_chunk", i, stream, _ptr(q, "q", _BF16, i, False),
+          _ptr(k_cache, "k_cache", _U8, i), _ptr(v_cache, "v_cache", _U8, i),
+          _ptr(block_tables, "block_tables", _I32S, i, False),
+          _ptr(context_lens, "context_lens", _I32S, i), _ptr(cu_seqlens_q, "cu_seqlens_q", _I32S, i),
+          _ptr(out, "out", _BF16, i, False), _ptr(lse, "lse", _F32S, i), n, tq, width,
+          table_stride if n > 1 else width, num_q_heads, num_kv_heads, head_dim, block_size, blocks,
+          k_scale, v_scale, head_dim ** -0.5 if softmax_scale is None else softmax_scale,
+          1 if causal else 0, qs, os_, cs, _ptr(workspace, "workspace", _BYTES, i),
+          0 if workspace is None else workspace.numel())
+    return out
+
+
+def _rows(t: torch.Tensor, name: str, like: tuple | None = None):
+    """(shape, row stride) of a [rows, columns] tensor whose rows are packed (a column view of a
+    wider buffer is fine)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    shape = tuple(t.shape)
+    if len(shape) != 2 or like is not None and shape != like:
+        raise ValueError(f"{name} must be {'[rows, columns]' if like is None else list(like)} (got {shape})")
+    stride, inner = t.stride()
+    if inner != 1 and shape[1] > 1:
+        raise ValueError(f"{name}'s rows must be packed")
+    return shape, stride if shape[0] > 1 else shape[1]
+
+
+def _group_outputs(shape, q, scales, device, stream):
+    """Codes and scales for rows of this shape, allocated where not given."""
+    m, k = shape
+    if q is None or scales is None:
+        with _on_stream(stream, device):
+            if q is None:
+                q = torch.empty((m, k), dtype=torch.uint8, device=device)
+            if scales is None:
+                scales = torch.empty((m, k // 128), dtype=torch.float32, device=device)
+    if tuple(q.shape) != (m, k) or scales.numel() != m * (k // 128):
+        raise ValueError(f"q must be [{m}, {k}], scales [{m}, {k // 128}]")
+    return q, scales
+
+
+def fp8_rms_norm_group_quant(x: torch.Tensor, weight: torch.Tensor | None, eps: float = 1e-6,
+                             residual: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                             scales: torch.Tensor | None = None,
+                             residual_out: torch.Tensor | None = None,
+                             norm_out: torch.Tensor | None = None, stream: int | None = None):
+    """RMS norm of x + residual, as E4M3 codes and 1x128 group scales in one pass: (q, scales,
+    residual_out).  residual_out is the bf16 sum that is normed (None without a residual); it may be
+    residual or x.  weight: bf16 [k], None for ones.  norm_out, if given, receives the normed rows in
+    bf16 (for the W8A16 tier); the codes are made of the rows before that rounding."""
+    shape, xs = _rows(x, "x")
+    k = shape[1]
+    if weight is not None and weight.numel() != k:
+        raise ValueError(f"weight must hold {k} values")
+    rs = ss = ns = k
+    if residual is not None:
+        _, rs = _rows(residual, "residual", shape)
+        if residual_out is None:
+            with _on_stream(stream, x.device):
+                residual_out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+        _, ss = _rows(residual_out, "residual_out", shape)
+    elif residual_out is not None:
+        raise ValueError("residual_out goes with a residual")
+    if norm_out is not None:
+        _, ns = _rows(norm_out, "norm_out", shape)
+    q, scales = _group_outputs(shape, q, scales, x.device, stream)
+    i = _gpu_index(x, "x")
+    _call("fp8_rms_norm_group_quant", i, stream, _ptr(x, "x", _BF16, i, False),
+          _ptr(residual, "residual", _BF16, i, False), _ptr(weight, "weight", _BF16, i), eps,
+          _ptr(residual_out, "residual_out", _BF16, i, False),
+          _ptr(norm_out, "norm_out", _BF16, i, False), _ptr(q, "q", _U8, i),
+          _ptr(scales, "scales", _F32S, i), shape[0], k, xs, rs, ss, ns)
+    return q, scales, residual_out
+
+
+def fp8_silu_mul_group_quant(gate: torch.Tensor, up: torch.Tensor, q: torch.Tensor | None = None,
+                             scales: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                             stream: int | None = None):
+    """silu(gate) * up, as E4M3 codes and 1x128 group scales in one pass: (q, scales).  gate and up may
+    be column halves of one buffer.  out, if given, receives the rows in bf16 (for the W8A16 tier);
+    the codes are made of the rows before that rounding."""
+    shape, gs = _rows(gate, "gate")
+    _, us = _rows(up, "up", shape)
+    os_ = shape[1]
+    if out is not None:
+        _, os_ = _rows(out, "out", shape)
+    q, scales = _group_outputs(shape, q, scales, gate.device, stream)
+    i = _gpu_index(gate, "gate")
+    _call("fp8_silu_mul_group_quant", i, stream, _ptr(gate, "gate", _BF16, i, False),
+          _ptr(up, "up", _BF16, i, False), _ptr(out, "out", _BF16, i, False), _ptr(q, "q", _U8, i),
+          _ptr(scales, "scales", _F32S, i), shape[0], shape[1], gs, us, os_)
+    return q, scales
 
 
 class KvCalibrator:

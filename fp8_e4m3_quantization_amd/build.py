@@ -15,7 +15,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libfp8q.so")
 SOURCES = ["fp8q_api.hip", "fp8q_quant.hip", "fp8q_gemm.hip", "fp8q_gemm_prefill.hip",
            "fp8q_gemv.hip", "fp8q_kv.hip", "fp8q_calib.hip", "fp8q_rope.hip",
-           "fp8q_attn_prefill.hip", "fp8q_attn_decode.hip"]
+           "fp8q_attn_prefill.hip", "fp8q_attn_decode.hip", "fp8q_attn_chunk.hip",
+           "fp8q_norm.hip"]
 ARCH = "gfx950"
 
 

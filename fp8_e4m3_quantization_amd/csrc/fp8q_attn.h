@@ -19,9 +19,6 @@ typedef unsigned v4u __attribute__((ext_vector_type(4)));
 // (prompts) and 0.4 ms (steps) at 2048, 14 and 6 ms at 8192, and would take minutes at 2^20.
 constexpr int kMostSeqs = 1 << 16;
 
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
-
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
 // A running reference of a softmax moves only when a score exceeds it by more than this many
@@ -46,6 +43,14 @@ __device__ __forceinline__ float max_over_rows(float v) {
 __device__ __forceinline__ float sum_over_rows(float v) {
   const v2u r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return sum_over_halves(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+}
+
+// Two E4M3 codes (low or high half of w) as two bf16, exact.
+template <bool kHigh>
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16(uint32_t w) {
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  const v2bf r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, kHigh);
+  return __builtin_bit_cast(uint32_t, r);
 }
 
 // Inclusive prefix sum over the wave: within rows of 16 lanes, then across them.

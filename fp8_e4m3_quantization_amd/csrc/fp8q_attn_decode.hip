@@ -89,14 +89,6 @@ struct Sums {
   }
 };
 
-// Two E4M3 codes (low or high half of w) as two bf16, exact.
-template <bool kHigh>
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16(uint32_t w) {
-  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-  const v2bf r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, kHigh);
-  return __builtin_bit_cast(uint32_t, r);
-}
-
 template <int N>
 __device__ __forceinline__ void load_bytes(const uint8_t* p, uint32_t* w) {
   if constexpr (N == 4) {

@@ -10,6 +10,24 @@
 
 namespace fp8q {
 
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// n / d for n < 2^31 by one high product: with l = ceil(log2 d) and m = floor(2^(31 + l) / d) + 1,
+// m d - 2^(31 + l) is at most d <= 2^l, so that m n / 2^(31 + l) lies between n / d and (n + 1) / d
+// below the next whole number.  m < 2^32 for every d >= 1.
+struct FastDiv {
+  uint32_t d, m, shift;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t by) : d(by), m(0), shift(0) {
+    while ((uint64_t(1) << shift) < by) ++shift;
+    m = uint32_t((uint64_t(1) << (31 + shift)) / by + 1);
+  }
+  __host__ __device__ __forceinline__ uint32_t div(uint32_t n) const {
+    return uint32_t((uint64_t(n) * m) >> 31 >> shift);
+  }
+};
+
 // ---------------------------------------------------------------- bf16 unpacking
 // A 32-bit word holds two bf16 values: element 0 in bits 15:0, element 1 in 31:16.
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }

@@ -51,8 +51,8 @@ int fp8q_version(void);
  * `start` as it begins executing and `stop` as it completes (hipExtLaunchKernelGGL), so
  * the events' elapsed time is that kernel's own duration.  Either may be NULL.  Every
  * entry point below enqueues exactly one kernel per call, except calls that enqueue
- * nothing (zero sizes, errors), the calibrator, attn_prefill and fp8_attn_decode (whose
- * first kernel is the timed one).  Always returns FP8Q_OK. */
+ * nothing (zero sizes, errors), the calibrator, attn_prefill, fp8_attn_decode and
+ * fp8_attn_chunk (whose first kernel is the timed one).  Always returns FP8Q_OK. */
 int fp8q_time_next_launch(hipEvent_t start, hipEvent_t stop);
 
 /* Measurement references (not steps of the path): kernels that the path's timings are read
@@ -92,6 +92,46 @@ int fp8q_reference_lds_stream(const void* src, int64_t span_bytes, int64_t total
  * Errors: FP8Q_EINVAL (k, m), FP8Q_ENULL, FP8Q_EALIGN, FP8Q_ELAUNCH. */
 int fp8_group_quant(const uint16_t* x, uint8_t* q, float* scales, int64_t m, int32_t k,
                     hipStream_t stream);
+
+/* ------------------- RMS norm with the residual's addition, to 1x128 groups
+ * The step before a projection ([decode] decode_w8a8_quant_act quantizes a normed activation), in
+ * one pass.  For every row r < m, in binary32:
+ *   h[j] = bf16_rne(x[r, j] + residual[r, j])   (residual NULL: x[r, j]); residual_out[r, j] = h[j]
+ *   y[j] = h[j] * weight[j] / sqrt(mean_j(h[j]^2) + eps)
+ *   per group of 128: scale and codes of y as fp8_group_quant makes them; norm_out[r, j] =
+ *   bf16_rne(y[j])
+ * y is not rounded to bf16 before it is quantized: codes and scales are those of the binary32 row,
+ * not of norm_out.  Rows are read once (twice beyond 32768 columns).
+ *   x, residual, residual_out, norm_out   device bf16 rows at their strides (elements, multiples of
+ *           8, at most 2^40), 16-byte aligned; residual_out goes with residual and may be it or x;
+ *           norm_out (for the W8A16 tier) may be NULL
+ *   weight  device bf16 [k], 16-byte aligned, or NULL (ones)
+ *   q       device uint8 [m, k], 16-byte aligned;  scales  device fp32 [m, k/128]
+ *   k > 0 and k % 128 == 0; m >= 0 (0 is a no-op), m * (k/128) < 2^31; 0 <= eps <= 1
+ * The squares' sum must stay within binary32.  A NaN makes its row NaN codes; so does a row of
+ * zeros with eps = 0.  Other outputs must not overlap inputs.
+ * Errors: FP8Q_EINVAL, FP8Q_ENULL, FP8Q_EALIGN, FP8Q_ELAUNCH. */
+int fp8_rms_norm_group_quant(const uint16_t* x, const uint16_t* residual, const uint16_t* weight,
+                             float eps, uint16_t* residual_out, uint16_t* norm_out, uint8_t* q,
+                             float* scales, int64_t m, int32_t k, int64_t x_stride,
+                             int64_t residual_stride, int64_t residual_out_stride,
+                             int64_t norm_out_stride, hipStream_t stream);
+
+/* --------------------------------- SiLU of the gate times up, to 1x128 groups
+ * The step between the gate and up projections and the down projection, in one pass.  For every
+ * row r < m, in binary32:
+ *   y[j] = gate[r, j] / (1 + exp(-gate[r, j])) * up[r, j]
+ *   per group of 128: scale and codes of y as fp8_group_quant makes them; out[r, j] =
+ *   bf16_rne(y[j]).  y is not rounded to bf16 before it is quantized.
+ *   gate, up, out   device bf16 rows at their strides (elements, multiples of 8, at most 2^40;
+ *           gate and up may be column halves of one buffer), 16-byte aligned; out may be NULL
+ *   q       device uint8 [m, k], 16-byte aligned;  scales  device fp32 [m, k/128]
+ *   k > 0 and k % 128 == 0; m >= 0 (0 is a no-op), m * (k/128) < 2^31
+ * The products must stay within binary32.  Outputs must not overlap inputs.
+ * Errors: FP8Q_EINVAL, FP8Q_ENULL, FP8Q_EALIGN, FP8Q_ELAUNCH. */
+int fp8_silu_mul_group_quant(const uint16_t* gate, const uint16_t* up, uint16_t* out, uint8_t* q,
+                             float* scales, int64_t m, int32_t k, int64_t gate_stride,
+                             int64_t up_stride, int64_t out_stride, hipStream_t stream);
 
 /* ---------------------------------------------- 128x128 weight block quant
  * [decode] module doc, NUMERICS: E4M3 weights carry one FP32 scale per 128x128 block;
@@ -470,6 +510,56 @@ int fp8_attn_decode(const uint16_t* q, const uint8_t* k_cache, const uint8_t* v_
                     float softmax_scale, int64_t q_stride, int64_t out_stride,
                     int64_t cache_stride, void* workspace, uint64_t workspace_bytes,
                     hipStream_t stream);
+
+/* ------------------------- attention of chunks of new tokens over the paged E4M3 cache
+ * [staging] module doc, as for fp8_attn_decode, for any number of new tokens a sequence: a chunk
+ * of a prompt, drafted tokens to verify, single steps, all in one batch.  Sequence s has the query
+ * rows cu_seqlens_q[s] .. cu_seqlens_q[s + 1] - 1 (Lq of them) and len = context_lens[s] cached
+ * positions, the new tokens' own among them as the last ones, written before the call; position p
+ * lies where fp8_attn_decode's does.  Query i sees the positions p < len, with `causal` those with
+ * p <= i + len - Lq (the last query sees every position).  With K, V the E4M3 values of KV head
+ * h / (Hq / Hkv):
+ *   s[i][p] = softmax_scale * k_scale * q[i][h] . K[p]
+ *   out[i][h] = bf16_rne( v_scale * sum_p exp(s[i][p]) V[p] / sum_p exp(s[i][p]) )
+ *   lse[i][h] = log sum_p exp(s[i][p])
+ * len is clamped to [0, max_blocks * block_size]; positions in a block outside [0, num_blocks)
+ * do not count; a query that sees no position gets zeros and lse = -infinity.  FP32 products, sums
+ * and statistics; out's weights are rounded to bf16, in its numerator and its denominator alike.
+ * What a query does not see does not reach it, NaN codes included; a NaN code of a value reaches
+ * that output of every query that sees it, however small its weight.  Results do not depend on the
+ * order in which workgroups run.
+ *   q, out      device bf16 rows at q_stride / out_stride elements, 16-byte aligned; rows of out
+ *               outside every sequence are left untouched
+ *   k_cache, v_cache  device uint8 pools of num_blocks * cache_stride bytes, 16-byte aligned
+ *   block_tables      device int32 [num_seqs, table_stride], the first max_blocks of each row used
+ *   context_lens      device int32 [num_seqs]
+ *   cu_seqlens_q      device int32 [num_seqs + 1], ascending from 0 to at most total_q (q's rows);
+ *                     entries are clamped to that range
+ *   lse         device fp32 [total_q, num_q_heads] or NULL
+ *   workspace   device memory of workspace_bytes >= fp8_attn_chunk_workspace_size's, 256-byte
+ *               aligned, of any content (nothing is kept in it from call to call); calls that
+ *               share one must not overlap in time; NULL is fine where the size is 0
+ *   head_dim in {64, 128, 256}; num_q_heads a multiple of num_kv_heads; total_q * num_q_heads <=
+ *   2^30; block_size > 0; num_seqs <= 65536; max_blocks * block_size <= 2^30; cache_stride >=
+ *   block_size*H*D, a multiple of 16; q / out strides multiples of 8; k_scale, v_scale in
+ *   [2^-64, 2^64]; 0 < softmax_scale <= 2^32.
+ * The scores must stay within binary32.  Outputs must not overlap inputs.
+ * Where the batch is too small to fill the GPU by its queries alone, histories are cut into parts:
+ * then a workspace is needed and two kernels are enqueued, the second joining the parts in order
+ * (batches of more than 256 sequences are never cut).
+ * fp8_attn_chunk_workspace_size: for the current device.
+ * Errors: FP8Q_EINVAL, FP8Q_ENULL, FP8Q_EALIGN, FP8Q_ELAUNCH. */
+int fp8_attn_chunk_workspace_size(int32_t num_seqs, int32_t total_q, int32_t num_q_heads,
+                                  int32_t num_kv_heads, int32_t head_dim, uint64_t* bytes);
+int fp8_attn_chunk(const uint16_t* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                   const int32_t* block_tables, const int32_t* context_lens,
+                   const int32_t* cu_seqlens_q, uint16_t* out, float* lse, int32_t num_seqs,
+                   int32_t total_q, int32_t max_blocks, int64_t table_stride,
+                   int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                   int32_t block_size, int64_t num_blocks, float k_scale, float v_scale,
+                   float softmax_scale, int32_t causal, int64_t q_stride, int64_t out_stride,
+                   int64_t cache_stride, void* workspace, uint64_t workspace_bytes,
+                   hipStream_t stream);
 
 /* ----------------------------------------------- online KV scale calibrator
  * [calib] module doc, PROVISIONAL_SCALE, Fp8KvCalibration::{new, observe, scales};
