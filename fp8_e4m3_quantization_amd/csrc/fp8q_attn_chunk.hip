@@ -178,8 +178,6 @@ __device__ __forceinline__ bool find_piece(const ChunkArgs& a, int u, Piece* pc)
 // What the kernel's two forms share: a piece, and the lane's place in it.
 template <int D>
 struct Work {
-  static constexpr int kLanes = D / 16;              // lanes that fetch a row of codes
-  static constexpr int kRowsAtOnce = 64 / kLanes;    // rows that a wave's copy of 1 KB holds
   const ChunkArgs& a;
   Piece pc;
   int kvh;
@@ -189,18 +187,6 @@ struct Work {
   // The id of a position's block (behind the last position: the last one's).
   __device__ __forceinline__ int block_at(int pos) const {
     return table[a.by_block.div(min(pos, pc.len - 1))];
-  }
-  // Where a position's row of this KV head lies in the pools.  A block that does not exist is
-  // replaced by the first one: what is read there does not count.
-  __device__ __forceinline__ int64_t row_at(int pos, int id) const {
-    pos = min(pos, pc.len - 1);
-    const int off = pos - int(a.by_block.div(pos)) * a.bs;
-    const bool good = uint32_t(id) < a.nblocks;
-    return (good ? id : 0) * a.cs + off * (int64_t(a.hkv) * D) + int64_t(kvh) * D;
-  }
-  // A copy of 16 bytes a lane into 1 KB of LDS.
-  static __device__ __forceinline__ void copy(const uint8_t* from, uint8_t* to) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from, (lds_void*)to, 16, 0, 0);
   }
   // Scores of positions that a row does not see, or that lie in blocks that do not exist, are
   // -infinity; s holds positions p0 .. p0 + 32 kBlocks - 1.
@@ -228,7 +214,8 @@ struct Work {
     for (int pos = first; pos < end; ++pos) {
       const int id = block_at(pos);
       if (uint32_t(id) >= a.nblocks) continue;
-      const uint8_t* v = a.vc + row_at(pos, id) + 4 * half;
+      const int off = pos - int(a.by_block.div(pos)) * a.bs;
+      const uint8_t* v = a.vc + id * a.cs + off * (int64_t(a.hkv) * D) + int64_t(kvh) * D + 4 * half;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -242,24 +229,80 @@ struct Work {
   }
 };
 
-// NaN codes of w become 0; `odd` is not 0 where there were any.
-__device__ __forceinline__ uint32_t without_nans(uint32_t w, uint32_t* odd) {
-  const uint32_t nan = e4m3_nan_bytes(w);
-  *odd |= nan;
-  return w & ~((nan >> 7) * 0xFFu);
+// Rows of codes that a lane copies into LDS, tile after tile: where the next ones lie.  A row's
+// block number is read one tile before the copy that it addresses.
+template <int D, int kRows>
+struct Rows {
+  static constexpr int kLanes = D / 16;              // lanes that copy a row
+  static constexpr int kAtOnce = 64 / kLanes;        // rows of a copy of 1 KB
+  int block[kRows], off[kRows];  // of the rows whose block number is read next
+  int id[kRows];                 // block numbers of the rows that are copied next
+  int at[kRows];                 // their places within the blocks
+  int step_blocks, step_off;     // from tile to tile
+
+  __device__ __forceinline__ void start(const ChunkArgs& a, int pos0, int row_step, int step) {
+    step_blocks = int(a.by_block.div(step));
+    step_off = step - step_blocks * a.bs;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const int pos = pos0 + j * row_step;
+      block[j] = int(a.by_block.div(pos));
+      off[j] = pos - block[j] * a.bs;
+    }
+  }
+  // Rows behind the last position come from its block: what lies there is masked.
+  __device__ __forceinline__ void read_ids(const ChunkArgs& a, const int32_t* table, int last_block) {
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      id[j] = table[min(block[j], last_block)];
+      at[j] = off[j];
+      off[j] += step_off;
+      const bool over = off[j] >= a.bs;
+      block[j] += step_blocks + (over ? 1 : 0);
+      off[j] -= over ? a.bs : 0;
+    }
+  }
+  // A block that does not exist is replaced by the first one: what is read there does not count.
+  __device__ __forceinline__ int64_t place(const ChunkArgs& a, int j) const {
+    const uint32_t good = uint32_t(id[j]) < a.nblocks ? id[j] : 0;
+    return int64_t(uint64_t(good) * uint32_t(a.cs) + uint64_t(uint32_t(at[j])) * uint32_t(a.hkv * D));
+  }
+};
+
+// A copy of 16 bytes a lane into 1 KB of LDS.
+__device__ __forceinline__ void copy16(const uint8_t* from, uint8_t* to) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from, (lds_void*)to, 16, 0, 0);
 }
 
-__device__ __forceinline__ v8bf e4m3x8_to_bf16(uint32_t lo, uint32_t hi) {
-  return __builtin_bit_cast(v8bf, v4u{e4m3x2_to_bf16<false>(lo), e4m3x2_to_bf16<true>(lo),
-                                      e4m3x2_to_bf16<false>(hi), e4m3x2_to_bf16<true>(hi)});
+// s_waitcnt's operand for vmcnt(n).
+constexpr int until_vmcnt(int n) { return (n & 15) | (n >> 4) << 14 | 0x0F70; }
+
+// The order of a turn: the score products with the weights and the widening of the keys between them,
+// then the value products with the widening of the values.
+template <int D>
+__device__ __forceinline__ void pair_up() {
+  constexpr int kMfma = 0x008, kVector = 0x002, kLdsRead = 0x100;
+  __builtin_amdgcn_sched_group_barrier(kLdsRead, 4, 0);
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(kVector, 10, 0);
+    __builtin_amdgcn_sched_group_barrier(kLdsRead, 1, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(kLdsRead, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(kVector, 8, 0);
+  }
 }
 
 template <int D>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chunk_kernel(const ChunkArgs a) {
-  // Two tiles each of keys and values in bf16, and one each of codes on their way there
-  __shared__ __attribute__((aligned(16))) uint16_t k0[kTileKeys * D], k1[kTileKeys * D];
-  __shared__ __attribute__((aligned(16))) uint16_t v0[kTileKeys * D], v1[kTileKeys * D];
-  __shared__ __attribute__((aligned(16))) uint8_t rk[kTileKeys * D], rv[kTileKeys * D];
+  // Four tiles of codes, keys then values
+  constexpr int kTileBytes = kTileKeys * D;
+  __shared__ __attribute__((aligned(16))) uint8_t t0[2 * kTileBytes], t1[2 * kTileBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t t2[2 * kTileBytes], t3[2 * kTileBytes];
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
@@ -280,7 +323,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
   }
   // Whether `x` holds in any lane of any wave; LDS is free before and after.
   auto any_of_all = [&](bool x) {
-    int* const flags = reinterpret_cast<int*>(k1);
+    int* const flags = reinterpret_cast<int*>(t3);
     const bool mine_any = __any(x);
     if (lane == 0) flags[wave] = mine_any;
     __syncthreads();
@@ -311,20 +354,18 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
   const int wave_least = __builtin_amdgcn_readfirstlane(mine + kWaveRows <= pc.rows ? pc.seen(a, query_of(mine)) : 0);
   const int all_see = __builtin_amdgcn_readfirstlane(pc.seen(a, query_of(0)));
 
-  // Queries, in the order in which a form reads keys: 16 values a step of two halves, or 32 a pair
-  // of steps.
   v8bf qf[D / 16];
   {
-    const uint16_t* src = a.q + int64_t(pc.q0 + my_query) * a.qs + int64_t(my_head) * D;
+    const uint16_t* src = a.q + int64_t(pc.q0 + my_query) * a.qs + int64_t(my_head) * D + 16 * half;
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s) {
-      const int at = few ? 32 * (s >> 1) + 16 * half + 8 * (s & 1) : 16 * s + 8 * half;
-      qf[s] = __builtin_bit_cast(v8bf, *reinterpret_cast<const uint4*>(src + at));
-    }
+    for (int s = 0; s < D / 16; ++s)
+      qf[s] = __builtin_bit_cast(v8bf, *reinterpret_cast<const uint4*>(src + 32 * (s >> 1) + 8 * (s & 1)));
   }
+  const int last_block = int(a.by_block.div(max(pc.len - 1, 0)));
   {
     bool bad = false;
-    const int first = a.by_block.div(pc.from * kTileKeys), last = pc.from < pc.to ? a.by_block.div(min(pc.to * kTileKeys, pc.len) - 1) : first - 1;
+    const int first = a.by_block.div(pc.from * kTileKeys);
+    const int last = pc.from < pc.to ? int(a.by_block.div(min(pc.to * kTileKeys, pc.len) - 1)) : first - 1;
     for (int i = first + tid; i <= last; i += kThreads) bad |= uint32_t(wk.table[i]) >= a.nblocks;
     wk.any_bad = any_of_all(bad);
   }
@@ -332,228 +373,183 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
   RowSums<D> sums;
   sums.clear();
   const float scale = a.scale_log2;
-  uint32_t odd = 0;  // not 0: NaN codes of values were left out of tiles that not all rows see
+  uint32_t odd = 0;  // not 0: NaN codes of values were left out, at positions from first_left_out on
+  int first_left_out = pc.from * kTileKeys;
+  const uint8_t* const kc = a.kc + int64_t(kvh) * D;
+  const uint8_t* const vc = a.vc + int64_t(kvh) * D;
 
   if (few) {
-    // Each wave takes every key_waves-th block of 32 positions: codes go to LDS, one block ahead, and
-    // are widened when they are read.
+    // Each wave takes every key_waves-th block of 32 positions, two blocks ahead in LDS.
+    const int lane = own_lane();
     constexpr int kCopies = D / 32;                        // copies of a block's keys, or values
-    const int f_row = lane / Work<D>::kLanes, f_place = lane % Work<D>::kLanes;
-    // order of the 16-byte chunks within a row: keys are read eight rows at a time, values rows
-    // 0..3 and 8..11 of 16 (or the others)
-    auto k_turn = [&](int r) { return D == 64 ? (r >> 1) & 3 : r & 7; };
-    auto v_turn = [&](int r) {
-      return D == 64 ? ((r >> 1) & 1) | ((r >> 2) & 2) : (r & 3) | ((r >> 1) & 4);
-    };
-    int ids[kCopies];
-    auto fetch_ids = [&](int n) {
-#pragma unroll
-      for (int j = 0; j < kCopies; ++j) ids[j] = wk.block_at(32 * n + j * Work<D>::kRowsAtOnce + f_row);
-    };
-    auto copy_block = [&](int n, uint8_t* ks, uint8_t* vs) {
-#pragma unroll
-      for (int j = 0; j < kCopies; ++j) {
-        const int r = j * Work<D>::kRowsAtOnce + f_row;
-        const int64_t at = wk.row_at(32 * n + r, ids[j]);
-        Work<D>::copy(a.kc + at + (f_place ^ k_turn(r)) * 16, ks + j * 1024);
-        Work<D>::copy(a.vc + at + (f_place ^ v_turn(r)) * 16, vs + j * 1024);
-      }
-    };
-    auto block = [&](int n, const uint8_t* ks, const uint8_t* vs) {
-      v16f s[1];
-#pragma unroll
-      for (int r = 0; r < 16; ++r) s[0][r] = 0.0f;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        const uint4 x = *reinterpret_cast<const uint4*>(ks + col * D + ((2 * c + half) ^ k_turn(col)) * 16);
-        s[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_bf16(x.x, x.y), qf[2 * c], s[0], 0, 0, 0);
-        s[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_bf16(x.z, x.w), qf[2 * c + 1], s[0], 0, 0, 0);
-      }
-      const bool edge = 32 * (n + 1) > all_see || wk.any_bad;
-      if (32 * (n + 1) > wave_least || wk.any_bad) wk.template mask<1>(s, 32 * n, limit);
-      const float base = sums.template move_to<1>(largest_score<1>(s) * scale, s, scale);
-#pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        const v8bf p = sums.weights(s[0], st, scale, base);
-        const int i16 = lane & 15, side = (lane >> 4) & 1;
-        const int r = 16 * st + 4 * half + ((i16 >> 1) & 3) + 8 * (i16 >> 3);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          typedef int v2i __attribute__((ext_vector_type(2)));
-          typedef __attribute__((address_space(3))) v2i lds_v2i;
-          v2u w = __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-              (lds_v2i*)(vs + r * D + ((2 * i + side) ^ v_turn(r)) * 16 + 8 * (i16 & 1))));
-          if (edge) w = v2u{without_nans(w[0], &odd), without_nans(w[1], &odd)};
-          sums.o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_bf16(w[0], w[1]), p, sums.o[i], 0, 0, 0);
-        }
-      }
-    };
-    uint8_t* const ks0 = reinterpret_cast<uint8_t*>(k0) + wave * 32 * D;
-    uint8_t* const vs0 = reinterpret_cast<uint8_t*>(v0) + wave * 32 * D;
-    uint8_t* const ks1 = reinterpret_cast<uint8_t*>(k1) + wave * 32 * D;
-    uint8_t* const vs1 = reinterpret_cast<uint8_t*>(v1) + wave * 32 * D;
+    typedef Rows<D, kCopies> R;
+    const int f_row = lane / R::kLanes, f_place = lane % R::kLanes;
     const int end = min(2 * pc.to, (pc.len + 31) / 32);
     int n = 2 * pc.from + key_wave;
+    R rows;
+    // Copies of the next block, after the block numbers of the one behind it: what waits for those
+    // need not wait for the copies.
+    auto copy_block = [&](uint8_t* ks, uint8_t* vs) {
+      int64_t at[kCopies];
+#pragma unroll
+      for (int j = 0; j < kCopies; ++j) at[j] = rows.place(a, j);
+      rows.read_ids(a, wk.table, last_block);
+#pragma unroll
+      for (int j = 0; j < kCopies; ++j) {
+        const int r = j * R::kAtOnce + f_row;
+        copy16(kc + at[j] + (f_place ^ key_turn<D>(r)) * 16, ks + j * 1024);
+        copy16(vc + at[j] + (f_place ^ value_turn<D>(r)) * 16, vs + j * 1024);
+      }
+    };
+    // Block n; with kEdge it may be seen in part.
+    auto block = [&](const uint8_t* ks, const uint8_t* vs, auto edge, int lane) {
+      constexpr bool kEdge = decltype(edge)::value;
+      v16f s[1];
+      code_scores<D, 1>(s, ks, qf, lane);
+      if (kEdge) wk.template mask<1>(s, 32 * n, limit);
+      const float base = sums.template move_to<1>(largest_score<1>(s) * scale, s, scale);
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+        sums.template add_values<kEdge>(vs, st, sums.weights(s[0], st, scale, base), &odd, lane);
+    };
+    // Waits for block n, takes it, and copies the one after the next into its place.
+    auto turn = [&](uint8_t* ks, uint8_t* vs, auto edge, int lane) {
+      asm volatile("" ::: "memory");
+      // this block's copies have landed: at most the next one's have not
+      if (n + key_waves < end) __builtin_amdgcn_s_waitcnt(until_vmcnt(2 * kCopies));
+      else __builtin_amdgcn_s_waitcnt(until_vmcnt(0));
+      asm volatile("" ::: "memory");
+      block(ks, vs, edge, lane);
+      if (n + 2 * key_waves < end) {
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this block has been read
+        asm volatile("" ::: "memory");
+        copy_block(ks, vs);
+      }
+      n += key_waves;
+    };
     if (n < end) {
-      fetch_ids(n);
-      copy_block(n, ks0, vs0);
-      fetch_ids(n + key_waves);
-      if (n + key_waves < end) copy_block(n + key_waves, ks1, vs1);
-      auto turn = [&](uint8_t* ks, uint8_t* vs) {
-        const bool more = n + key_waves < end;
-        fetch_ids(n + 2 * key_waves);
-        asm volatile("" ::: "memory");
-        // the copies of this block have landed: at most those of the next one, and its ids, have not
-        if (more) __builtin_amdgcn_s_waitcnt((2 * kCopies & 15) | (2 * kCopies >> 4) << 14 | 0x0F70);
-        else __builtin_amdgcn_s_waitcnt(0x0F70);
-        asm volatile("" ::: "memory");
-        block(n, ks, vs);
-        if (n + 2 * key_waves < end) {
-          __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this block has been read
-          asm volatile("" ::: "memory");
-          copy_block(n + 2 * key_waves, ks, vs);
-        }
-        n += key_waves;
-        return more;
-      };
-      while (turn(ks0, vs0) && turn(ks1, vs1)) {}
+      const int mine32 = wave * 32 * D;
+      const int whole = wk.any_bad ? 0 : min(end, all_see / 32);  // blocks that all rows see
+      first_left_out = max(first_left_out, 32 * whole);
+      rows.start(a, 32 * n + f_row, R::kAtOnce, 32 * key_waves);
+      rows.read_ids(a, wk.table, last_block);
+      copy_block(t0 + mine32, t1 + mine32);
+      if (n + key_waves < end) copy_block(t2 + mine32, t3 + mine32);
+      int odd_turn = 0;
+      while (n < whole) {
+        turn(t0 + mine32, t1 + mine32, std::false_type{}, lane);
+        odd_turn = 1;
+        if (n >= whole) break;
+        turn(t2 + mine32, t3 + mine32, std::false_type{}, lane);
+        odd_turn = 0;
+      }
+      while (n < end) {
+        const int lane = own_lane();
+        turn((odd_turn ? t2 : t0) + mine32, (odd_turn ? t3 : t1) + mine32, std::true_type{}, lane);
+        odd_turn ^= 1;
+      }
     }
   } else {
     // All waves go over all positions, 64 at a time.
-    constexpr int kCopies = D / 64;                        // 1 KB copies of a wave and tile
-    const int f_row = lane / Work<D>::kLanes, f_place = lane % Work<D>::kLanes;
-    int ids[kCopies];          // of the keys' next tile
-    int64_t at[kCopies];       // rows of the values' next tile
-    int next_k = pc.from, next_ids = pc.from;              // tiles
-    auto fetch_ids = [&]() {
+    const int lane = own_lane();
+    constexpr int kCopies = D / 64;                        // 1 KB copies of a wave of a tile's keys, or values
+    typedef Rows<D, kCopies> R;
+    const int f_row = wave * kCopies * R::kAtOnce + lane / R::kLanes, f_place = lane % R::kLanes;
+    R rows;
+    rows.start(a, pc.from * kTileKeys + f_row, R::kAtOnce, kTileKeys);
+    // Copies of the next tile, after the block numbers of the one behind it: what waits for those
+    // need not wait for the copies.
+    auto copy_next = [&](uint8_t* to) {
+      int64_t at[kCopies];
 #pragma unroll
-      for (int j = 0; j < kCopies; ++j)
-        ids[j] = wk.block_at(next_ids * kTileKeys + (wave * kCopies + j) * Work<D>::kRowsAtOnce + f_row);
-      ++next_ids;
-    };
-    // Copies of the next tile of values, whose place the keys' copies left, and of the one of keys
-    // after it.
-    auto copy_values = [&]() {
-#pragma unroll
-      for (int j = 0; j < kCopies; ++j)
-        Work<D>::copy(a.vc + at[j] + f_place * 16, rv + (wave * kCopies + j) * 1024);
-    };
-    auto copy_keys = [&]() {
+      for (int j = 0; j < kCopies; ++j) at[j] = rows.place(a, j);
+      rows.read_ids(a, wk.table, last_block);
 #pragma unroll
       for (int j = 0; j < kCopies; ++j) {
-        at[j] = wk.row_at(next_k * kTileKeys + (wave * kCopies + j) * Work<D>::kRowsAtOnce + f_row, ids[j]);
-        Work<D>::copy(a.kc + at[j] + f_place * 16, rk + (wave * kCopies + j) * 1024);
+        const int r = f_row + j * R::kAtOnce;
+        copy16(kc + at[j] + (f_place ^ key_turn<D>(r)) * 16, to + (wave * kCopies + j) * 1024);
+        copy16(vc + at[j] + (f_place ^ value_turn<D>(r)) * 16, to + kTileBytes + (wave * kCopies + j) * 1024);
       }
-      ++next_k;
-    };
-    // A wave widens the codes that it copied: eight of a row a lane.
-    constexpr int kWide = 64 / (D / 8);                    // rows at a time
-    const int w_row = lane / (D / 8), w_chunk = lane % (D / 8);
-    auto widen = [&](const uint8_t* codes, uint16_t* to, auto chunk_of, bool clean) {
-#pragma unroll
-      for (int j = 0; j < 2 * kCopies; ++j) {
-        const int r = wave * kCopies * Work<D>::kRowsAtOnce + j * kWide + w_row;
-        uint2 x = *reinterpret_cast<const uint2*>(codes + r * D + w_chunk * 8);
-        if (clean) x = make_uint2(without_nans(x.x, &odd), without_nans(x.y, &odd));
-        *reinterpret_cast<v8bf*>(to + r * D + chunk_of(r, w_chunk) * 8) = e4m3x8_to_bf16(x.x, x.y);
-      }
-    };
-    auto widen_keys = [&](uint16_t* to) { widen(rk, to, [](int r, int c) { return k_chunk<D>(r, c); }, false); };
-    auto widen_values = [&](uint16_t* to, bool clean) {
-      widen(rv, to, [](int r, int c) { return v_chunk<D>(r, c); }, clean);
     };
     const int tiles = pc.to - pc.from;
     const int whole = wk.any_bad ? 0 : all_see / kTileKeys - pc.from;   // tiles that all rows see
-    auto landed = [&]() {
-      asm volatile("" ::: "memory");
-      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's copies
-      asm volatile("" ::: "memory");
-    };
     float base = 0.0f;
-    auto scores = [&](int t, v16f* s, const uint16_t* kt) {
-      tile_scores<D>(s, kt, qf);
+    // At the barrier of tile t all waves' copies of tile t + 1 have landed (at most those of t + 2
+    // have not), and the tile before t has been read by all: tile t + 3 takes its place.
+    auto next_tile = [&](uint8_t* free) {
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(until_vmcnt(2 * kCopies));
+      __syncthreads();
+      copy_next(free);
+    };
+    auto scores = [&](int t, v16f* s, const uint8_t* kt, int lane) {
+      code_scores<D, 2>(s, kt, qf, lane);
       const int p0 = (pc.from + t) * kTileKeys;
       if (p0 + kTileKeys > wave_least || wk.any_bad) wk.template mask<2>(s, p0, limit);
       base = sums.template move_to<2>(largest_score<2>(s) * scale, s, scale);
     };
-    // At the barrier of tile t of the piece the other waves' codes are wide, and the places of the
-    // keys of tile t and of the values before them are free: this wave widens its codes of the keys of
-    // tile t + 2 and of the values of t + 1, and starts the copies of the next ones.
-    auto next_tile = [&](uint16_t* k_free, uint16_t* v_free, bool clean) {
-      landed();
-      __syncthreads();
-      widen_keys(k_free);
-      widen_values(v_free, clean);
-      asm volatile("" ::: "memory");
-      copy_values();
-      copy_keys();
-      fetch_ids();
-    };
     // Tile t, whose scores are s, while the whole tiles last: the scores of t + 1 (matrix cores) beside
     // the weights of t (vector ALUs), then the values of t beside the largest of the new scores.
-    auto turn = [&](const v16f* s, v16f* next, const uint16_t* kn, const uint16_t* vt,
-                    uint16_t* k_free, uint16_t* v_free) {
-      next_tile(k_free, v_free, false);
-      tile_scores<D>(next, kn, qf);
+    auto turn = [&](const v16f* s, v16f* next, const uint8_t* here, const uint8_t* then, uint8_t* free) {
+      next_tile(free);
+      code_scores<D, 2>(next, then, qf, lane);
       v8bf p[4];
 #pragma unroll
       for (int st = 0; st < 4; ++st) p[st] = sums.weights(s[st >> 1], st & 1, scale, base);
 #pragma unroll
-      for (int st = 0; st < 4; ++st) sums.add_values(vt, st, p[st]);
-      base = sums.template move_to<2>(largest_score<2>(next) * scale, next, scale);
+      for (int st = 0; st < 4; ++st) sums.template add_values<false>(here + kTileBytes, st, p[st], &odd, lane);
+      const float top = largest_score<2>(next);
+      if constexpr (D == 128) pair_up<D>();
+      base = sums.template move_to<2>(top * scale, next, scale);
     };
     if (tiles > 0) {
       v16f sa[2];
-      fetch_ids();
-      copy_keys();           // keys of tile 0
-      fetch_ids();
-      copy_values();         // values of tile 0
-      landed();
-      widen_keys(k0);
-      widen_values(v0, 0 >= whole);
+      rows.read_ids(a, wk.table, last_block);
+      copy_next(t0);
+      copy_next(t1);
+      copy_next(t2);
       asm volatile("" ::: "memory");
-      copy_keys();           // keys of tile 1 (behind the last one: of the last position again)
-      fetch_ids();
-      landed();
-      widen_keys(k1);
-      asm volatile("" ::: "memory");
-      copy_values();         // values of tile 1
-      copy_keys();           // keys of tile 2
-      fetch_ids();
+      __builtin_amdgcn_s_waitcnt(until_vmcnt(4 * kCopies));
       __syncthreads();
-      scores(0, sa, k0);
+      scores(0, sa, t0, lane);
       int t = 0;
-      for (; t + 2 < whole && t + 2 < tiles; t += 2) {
+      while (t + 2 < whole && t + 2 < tiles) {
         v16f sb[2];
-        turn(sa, sb, k1, v0, k0, v1);
-        turn(sb, sa, k0, v1, k1, v0);
+        turn(sa, sb, t0, t1, t3);
+        turn(sb, sa, t1, t2, t0);
+        t += 2;
+        if (!(t + 2 < whole && t + 2 < tiles)) break;
+        turn(sa, sb, t2, t3, t1);
+        turn(sb, sa, t3, t0, t2);
+        t += 2;
       }
+      first_left_out += t * kTileKeys;
       for (; t < tiles; ++t) {  // the last tiles, among them those that are seen in part
-        const uint16_t *kn = t & 1 ? k0 : k1, *vt = t & 1 ? v1 : v0;
-        next_tile(t & 1 ? k1 : k0, t & 1 ? v0 : v1, t + 1 >= whole);
+        const int lane = own_lane();
+        auto slot_of = [&](int i) { return i & 2 ? i & 1 ? t3 : t2 : i & 1 ? t1 : t0; };
+        next_tile(slot_of(t + 3));
 #pragma unroll
-        for (int st = 0; st < 4; ++st) sums.add_values(vt, st, sums.weights(sa[st >> 1], st & 1, scale, base));
+        for (int st = 0; st < 4; ++st)
+          sums.template add_values<true>(slot_of(t) + kTileBytes, st, sums.weights(sa[st >> 1], st & 1, scale, base), &odd, lane);
         __builtin_amdgcn_sched_barrier(0);
-        if (t + 1 < tiles) scores(t + 1, sa, kn);
+        if (t + 1 < tiles) scores(t + 1, sa, slot_of(t + 1), lane);
       }
+      __builtin_amdgcn_s_waitcnt(until_vmcnt(0));  // copies behind the last tile: LDS is used again
     }
   }
 
   // NaN codes that were left out reach the rows that see them.
   __syncthreads();
-  if (any_of_all(odd != 0) && key_wave == 0) {
-    const int first = wk.any_bad ? pc.from : max(pc.from, all_see / kTileKeys);
-    wk.take_nans(sums, first * kTileKeys, limit);
-  }
+  if (any_of_all(odd != 0) && key_wave == 0) wk.take_nans(sums, first_left_out, limit);
 
   float ref = sums.ref, total = sum_over_halves(sums.sum), of_rounded = sum_over_halves(sums.rounded[0]);
   v16f* const o = sums.o;
   // Waves that took different positions of the same rows add up in pairs, through LDS.
-  float4* const s_stats = reinterpret_cast<float4*>(rk);
+  float4* const s_stats = reinterpret_cast<float4*>(t2);
   for (int n = key_waves / 2; n >= 1; n /= 2) {
     __syncthreads();
     const int to = wave & (row_waves * n - 1);
-    float* const s_o = reinterpret_cast<float*>(to == 0 ? k0 : k1);
+    float* const s_o = reinterpret_cast<float*>(to == 0 ? t0 : t1);
     if (key_wave >= n && key_wave < 2 * n) {
 #pragma unroll
       for (int i = 0; i < D / 32; ++i)
@@ -715,7 +711,8 @@ extern "C" int fp8_attn_chunk(const uint16_t* q, const uint8_t* k_cache, const u
   if (q_stride < eq || out_stride < eq || q_stride > (int64_t(1) << 30) ||
       out_stride > (int64_t(1) << 30) || table_stride > (int64_t(1) << 40))
     return FP8Q_EINVAL;
-  if (cache_stride < int64_t(block_size) * ek || num_blocks > (int64_t(1) << 62) / cache_stride)
+  if (cache_stride < int64_t(block_size) * ek || num_blocks > (int64_t(1) << 62) / cache_stride ||
+      cache_stride >= (int64_t(1) << 32))
     return FP8Q_EINVAL;
   if (!(k_scale >= 0x1p-64f && k_scale <= 0x1p64f) || !(v_scale >= 0x1p-64f && v_scale <= 0x1p64f) ||
       !(softmax_scale > 0.0f && softmax_scale <= 0x1p32f))

@@ -1,9 +1,17 @@
-// fp8q_attn_tile.h -- the steps of attention over a tile of bf16 keys and values in LDS, for a wave
-// that owns 32 query rows: lane l has row l % 32, half l / 32 of the keys of every score tile.
+// fp8q_attn_tile.h -- the steps of attention over E4M3 keys and values in LDS, for a wave that owns 32
+// query rows: lane l has row l % 32, half l / 32 of the keys of every 32.
 #pragma once
 #include "fp8q_attn.h"
 
 namespace fp8q {
+
+// The lane's number as the compiler may not know it: addresses made of it are not shared with other
+// code, where they would take registers from the loops between.
+__device__ __forceinline__ int own_lane() {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
 
 constexpr int kTileKeys = 64;
 constexpr int kWaveRows = 32;
@@ -11,51 +19,63 @@ constexpr float kFar = 0x1p27f;  // a reference whose rounding (2^3) still leave
 
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
-typedef __attribute__((address_space(3))) v4s lds_v4s;
 
-// Order of the 16-byte chunks within a row of a tile in LDS.  K is read 16 rows at a time, one
-// chunk each; V (transposing read) four rows at a time, 64 bytes each: both then touch every bank
-// once.
+// Order of the 16-byte chunks within a row of codes in LDS: the place of chunk c of row r is
+// c ^ key_turn(r), or value_turn(r).  Keys are read eight rows at a time, values rows 0..3 and 8..11
+// of 16 (or the others) at a time: each then touches every bank once.
 template <int D>
-__device__ __forceinline__ int k_chunk(int row, int c) {
-  return D == 64 ? c ^ ((row >> 1) & 7) : c ^ (row & 15);
-}
+__device__ __forceinline__ int key_turn(int r) { return D == 64 ? (r >> 1) & 3 : r & 7; }
 template <int D>
-__device__ __forceinline__ int v_chunk(int row, int c) {
-  return D == 64 ? c ^ (((row >> 1) & 1) << 2) : c ^ ((row & 3) << 2);
+__device__ __forceinline__ int value_turn(int r) {
+  return D == 64 ? ((r >> 1) & 1) | ((r >> 2) & 2) : (r & 3) | ((r >> 1) & 4);
 }
 
-// S^T of a tile: s[b] holds keys 32 b .. 32 b + 31.
-template <int D>
-__device__ __forceinline__ void tile_scores(v16f* s, const uint16_t* kt, const v8bf* qf) {
-  const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
+__device__ __forceinline__ v8bf e4m3x8_to_bf16(uint32_t lo, uint32_t hi) {
+  return __builtin_bit_cast(v8bf, v4u{e4m3x2_to_bf16<false>(lo), e4m3x2_to_bf16<true>(lo),
+                                      e4m3x2_to_bf16<false>(hi), e4m3x2_to_bf16<true>(hi)});
+}
+
+// S^T of 32 kBlocks keys whose codes lie in LDS; a pair of steps takes 32 values of a row, 16 for each
+// half, so the queries' fragments 2 c and 2 c + 1 hold values 32 c + 16 half .. + 7 and + 8 .. + 15.
+template <int D, int kBlocks>
+__device__ __forceinline__ void code_scores(v16f* s, const uint8_t* ks, const v8bf* qf, int lane) {
+  const int col = lane & 31, half = lane >> 5;
 #pragma unroll
-  for (int b = 0; b < 2; ++b)
+  for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
     for (int r = 0; r < 16; ++r) s[b][r] = 0.0f;
 #pragma unroll
-  for (int st = 0; st < D / 16; ++st)
+  for (int c = 0; c < D / 32; ++c) {
+    uint4 x[kBlocks];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int r = 32 * b + col;
-      const v8bf kf = __builtin_bit_cast(
-          v8bf, *reinterpret_cast<const uint4*>(kt + r * D + k_chunk<D>(r, 2 * st + half) * 8));
-      s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[st], s[b], 0, 0, 0);
-    }
+    for (int b = 0; b < kBlocks; ++b)
+      x[b] = *reinterpret_cast<const uint4*>(ks + (32 * b + col) * D + ((2 * c + half) ^ key_turn<D>(col)) * 16);
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b)
+      s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_bf16(x[b].x, x[b].y), qf[2 * c], s[b], 0, 0, 0);
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b)
+      s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_bf16(x[b].z, x[b].w), qf[2 * c + 1], s[b], 0, 0, 0);
+  }
 }
 
-// V^T of 16 keys (step st of the tile) and 32 values (block i), in the order of the weights.
+// Codes of V^T of 16 keys (step st of those in LDS) and 32 values (block i): keys 4h..4h+3 and
+// 8+4h..8+4h+3 for lane half h, the order in which the lane holds their scores.
 template <int D>
-__device__ __forceinline__ v4u value_frag(const uint16_t* vt, int st, int i) {
-  const int lane = threadIdx.x & 63, half = lane >> 5;
-  const int i16 = lane & 15, side = (lane >> 4) & 1;
-  const int ra = 16 * st + 4 * half + (i16 >> 2), c = 4 * i + 2 * side + ((i16 & 3) >> 1);
-  const int within = 4 * (i16 & 1);
-  const v2u lo = __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-      (lds_v4s*)(vt + ra * D + v_chunk<D>(ra, c) * 8 + within)));
-  const v2u hi = __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-      (lds_v4s*)(vt + (ra + 8) * D + v_chunk<D>(ra + 8, c) * 8 + within)));
-  return v4u{lo[0], lo[1], hi[0], hi[1]};
+__device__ __forceinline__ v2u value_codes(const uint8_t* vs, int st, int i, int lane) {
+  typedef int v2i __attribute__((ext_vector_type(2)));
+  typedef __attribute__((address_space(3))) v2i lds_v2i;
+  const int half = lane >> 5, i16 = lane & 15, side = (lane >> 4) & 1;
+  const int r = 4 * half + ((i16 >> 1) & 3) + 8 * (i16 >> 3);
+  return __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+      (lds_v2i*)(vs + (16 * st + r) * D + ((2 * i + side) ^ value_turn<D>(r)) * 16 + 8 * (i16 & 1))));
+}
+
+// NaN codes of w become 0; `odd` is not 0 where there were any.
+__device__ __forceinline__ uint32_t without_nans(uint32_t w, uint32_t* odd) {
+  const uint32_t nan = e4m3_nan_bytes(w);
+  *odd |= nan;
+  return w & ~((nan >> 7) * 0xFFu);
 }
 
 // The largest of kBlocks times 32 scores of a row, before their scale.
@@ -136,11 +156,15 @@ struct RowSums {
     rounded = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(ones, __builtin_bit_cast(v4s, v2u{w[2], w[3]}), rounded, 0, 0, 0);
     return __builtin_bit_cast(v8bf, v4u{w[0], w[1], w[2], w[3]});
   }
-  __device__ __forceinline__ void add_values(const uint16_t* vt, int st, v8bf p) {
+  // o^T += V^T P^T over 16 keys.  With kClean NaN codes are left out (and `odd` tells).
+  template <bool kClean>
+  __device__ __forceinline__ void add_values(const uint8_t* vs, int st, v8bf p, uint32_t* odd, int lane) {
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-      o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, value_frag<D>(vt, st, i)), p,
-                                                     o[i], 0, 0, 0);
+    for (int i = 0; i < D / 32; ++i) {
+      v2u w = value_codes<D>(vs, st, i, lane);
+      if (kClean) w = v2u{without_nans(w[0], odd), without_nans(w[1], odd)};
+      o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_bf16(w[0], w[1]), p, o[i], 0, 0, 0);
+    }
   }
 };
 
