@@ -22,9 +22,14 @@ namespace {
 constexpr int kTileRows = 128;   // rows (query, head of a KV head's group) of a workgroup
 constexpr int kThreads = 256;
 constexpr int kSplitSeqs = 256;  // batches of more sequences are not split along the positions
+constexpr int kFewRows = 64;     // so many rows of a sequence and KV head at most: another form
 constexpr int kMinPart = 4;      // tiles of positions of a part, at least
-constexpr int kFewRows = 64;     // tiles of so many rows at most divide positions among the waves
-constexpr float kFewCost = 0.6f; // time of their tile of positions, of another's
+constexpr int kMinFewPart = 2;   // the same of few rows
+// Times, in that of a tile of positions of a workgroup of many rows that shares its compute unit:
+constexpr float kFewCost = 0.6f;    // a tile of positions of few rows, for each KV head
+constexpr float kAloneCost = 0.6f;  // a tile of a workgroup alone on its compute unit
+constexpr float kPieceCost = 2.0f;  // a workgroup's start and end
+constexpr float kJoinCost = 0.011f; // a part's sums, written and read again
 
 struct ChunkArgs {
   const uint16_t* q;
@@ -32,146 +37,207 @@ struct ChunkArgs {
   const int32_t *tables, *lens, *cu;
   uint16_t* out;
   float* lse;     // [tq, hq] or NULL
-  float* sums;    // [hkv][slots][kTileRows][D]: sums of weighted values of parts
-  float4* stats;  // [hkv][slots][kTileRows]: reference (log2 units), sums of the weights and of the
+  float* sums;    // [hkv * slots][kTileRows][D]: sums of weighted values of parts
+  float4* stats;  // [hkv * slots][kTileRows]: reference (log2 units), sums of the weights and of the
                   // rounded ones
-  int4* pieces;   // [hkv][slots]: first query row, first row, rows, part | parts << 16
+  int4* parts;    // [hkv * slots], and one more: the number of those in use
   int64_t ts, qs, os, cs, nblocks;
   FastDiv by_group, by_block;
   int seqs, width, tq, hq, hkv, group, bs, causal;
-  int slots;      // pieces of a KV head when sequences are split; 0: they are not
+  int most_heads;  // KV heads that a piece of few rows takes at most: 1, 2 or 4
+  int slots;       // pieces of a KV head when sequences are split; 0: they are not
+  float resident;  // pieces of a KV head that run at once
   float scale_log2, v_scale;
 };
 
-// A piece of work: a tile of rows of one sequence and KV head, and the steps that it goes over.
+// A sequence, whatever the lists hold: its first query row, queries and positions; and how its rows
+// of a KV head are worked on.
+struct Seq {
+  int q0, lq, len;
+  __device__ __forceinline__ Seq(const ChunkArgs& a, int s) {
+    q0 = lq = len = 0;
+    if (s >= a.seqs) return;
+    const int from = min(max(a.cu[s], 0), a.tq);
+    q0 = from;
+    lq = min(max(a.cu[s + 1], from), a.tq) - from;
+    len = min(max(a.lens[s], 0), a.width * a.bs);
+  }
+  __device__ __forceinline__ int rows(const ChunkArgs& a) const { return lq * a.group; }
+  __device__ __forceinline__ bool few(const ChunkArgs& a) const { return rows(a) <= kFewRows; }
+  __device__ __forceinline__ int tiles(const ChunkArgs& a) const { return (rows(a) + kTileRows - 1) / kTileRows; }
+  // tiles of positions
+  __device__ __forceinline__ int steps() const { return lq > 0 ? (len + kTileKeys - 1) / kTileKeys : 0; }
+  // KV heads of a piece: a token's heads lie side by side in the pools, and one head's rows read
+  // alone stream slower
+  __device__ __forceinline__ int heads(const ChunkArgs& a) const {
+    return few(a) ? min(a.most_heads, rows(a) > kWaveRows ? 2 : 4) : 1;
+  }
+  // Time of a tile of positions in a piece.
+  __device__ __forceinline__ float tile_cost(const ChunkArgs& a) const {
+    return few(a) ? kFewCost * float(heads(a)) : 1.0f;
+  }
+  // Parts that the positions may be cut into.
+  __device__ __forceinline__ int cap(const ChunkArgs& a) const {
+    return max(steps() / (few(a) ? kMinFewPart : kMinPart), 1);
+  }
+};
+
+// Parts, `cap` at most, of a sequence whose pieces take `cost` when one takes at most about `most`.  The
+// same arithmetic in every workgroup: all agree.
+__device__ __forceinline__ float parts_of(float cost, int cap, float most) {
+  return fmaxf(fminf(__builtin_ceilf(cost * __builtin_amdgcn_rcpf(most)), float(cap)), 1.0f);
+}
+
+__device__ __forceinline__ float wave_sum_f(float v) {
+  for (int m = 1; m < 64; m *= 2) v += __shfl_xor(v, m);
+  return v;
+}
+__device__ __forceinline__ int last_lane(int v) { return __builtin_amdgcn_readlane(v, 63); }
+
+// A piece of work: a tile of rows of one sequence and KV head, or the few rows of a sequence for
+// several KV heads; and the positions that it goes over.
 struct Piece {
   int seq, q0, lq, len;  // the sequence's first query row, queries and positions
   int row0, rows;        // the tile's first row of the sequence's, and how many
+  int kvh, heads;        // the first KV head, and how many
   int part, parts, from, to;  // tiles of positions [from, to)
+  int slot;              // where the sums of a part go
   // positions [0, seen(i)) are seen by query i
   __device__ __forceinline__ int seen(const ChunkArgs& a, int i) const {
     return a.causal ? min(max(i + len - lq + 1, 0), len) : len;
   }
 };
 
-// Sequence s: its first query row, queries and positions, whatever the lists hold.
-__device__ __forceinline__ void seq_of(const ChunkArgs& a, int s, int* q0, int* lq, int* len) {
-  const int from = min(max(a.cu[s], 0), a.tq);
-  *q0 = from;
-  *lq = min(max(a.cu[s + 1], from), a.tq) - from;
-  *len = min(max(a.lens[s], 0), a.width * a.bs);
-}
-
-__device__ __forceinline__ int tiles_of(const ChunkArgs& a, int lq) {
-  return (lq * a.group + kTileRows - 1) / kTileRows;
-}
-__device__ __forceinline__ int key_tiles(int positions) { return (positions + kTileKeys - 1) / kTileKeys; }
-
-// Parts of a sequence of `steps` tiles of positions when a piece takes at most about `most` (in time
-// of a tile of many rows).  The same arithmetic in every workgroup: all agree.
-__device__ __forceinline__ int parts_of(const ChunkArgs& a, int lq, int steps, float most) {
-  const float cost = float(steps) * (lq * a.group <= kFewRows ? kFewCost : 1.0f);
-  const int n = int(__builtin_ceilf(cost * __builtin_amdgcn_rcpf(most)));
-  return max(min(n, steps / kMinPart), 1);
-}
-
-__device__ __forceinline__ int wave_sum(int v) { return __builtin_amdgcn_readlane(wave_prefix(v), 63); }
-
-// Piece `u` of a KV head's, or false.  Where all sequences' tiles together are fewer than the
-// slots, each sequence's positions are cut into parts: as few as a limit on the steps of a piece
-// makes, the smallest limit whose pieces the slots hold.
-__device__ __forceinline__ bool find_piece(const ChunkArgs& a, int u, Piece* pc) {
+// The limit on the time of a piece, from which the parts of each sequence follow (none: 1e9).  64 limits
+// are tried, a lane each: from the time that all pieces would take in equal shares on, in steps of
+// 2.5 %; the least estimated time wins.  All threads call it; lds: 4 KB.
+__device__ __forceinline__ float find_limit(const ChunkArgs& a, const Seq& first, uint8_t* lds) {
   const int lane = threadIdx.x & 63;
-  int tile = 0, tiles = 0, parts = 1, part = 0;
-  if (a.seqs > kSplitSeqs) {
-    bool found = false;
-    for (int s0 = 0; s0 < a.seqs && !found; s0 += 64) {
-      int q0 = 0, lq = 0, len = 0;
-      if (s0 + lane < a.seqs) seq_of(a, s0 + lane, &q0, &lq, &len);
-      const int n = tiles_of(a, lq), upto = wave_prefix(n), all = __builtin_amdgcn_readlane(upto, 63);
-      if (u < all) {
-        const int j = __builtin_ctzll(__ballot(upto > u));
-        pc->seq = s0 + j;
-        pc->q0 = __builtin_amdgcn_readlane(q0, j);
-        pc->lq = __builtin_amdgcn_readlane(lq, j);
-        pc->len = __builtin_amdgcn_readlane(len, j);
-        tiles = __builtin_amdgcn_readlane(n, j);
-        u -= __builtin_amdgcn_readlane(upto, j) - tiles;
-        found = true;
-      } else {
-        u -= all;
-      }
-    }
-    if (!found) return false;
-    tile = tiles - 1 - u;
-  } else {
-    constexpr int kSets = kSplitSeqs / 64;
-    int q0[kSets] = {}, lq[kSets] = {}, len[kSets] = {}, n[kSets] = {}, steps[kSets] = {};
-    int all = 0, longest = 0;
-#pragma unroll
-    for (int c = 0; c < kSets; ++c) {
-      if (c * 64 >= a.seqs) continue;
-      if (c * 64 + lane < a.seqs) seq_of(a, c * 64 + lane, &q0[c], &lq[c], &len[c]);
-      n[c] = tiles_of(a, lq[c]);
-      steps[c] = lq[c] > 0 ? key_tiles(len[c]) : 0;
-      all += wave_sum(n[c]);
-      longest = max(longest, int(max_over_wave(float(steps[c]))));
-    }
-    float most = 1e9f;
-    if (all < a.slots && longest > kMinPart) {
-      auto pieces = [&](float limit) {
-        int sum = 0;
-#pragma unroll
-        for (int c = 0; c < kSets; ++c)
-          if (c * 64 < a.seqs) sum += n[c] * parts_of(a, lq[c], steps[c], limit);
-        return wave_sum(sum);
-      };
-      // (one part each at the upper end, however the reciprocal is rounded)
-      float lo = 1.0f, hi = 2.0f * float(longest);
-      if (pieces(lo) <= a.slots) {
-        hi = lo;
-      } else {
-        for (int i = 0; i < 12; ++i) {
-          const float mid = 0.5f * (lo + hi);
-          if (pieces(mid) <= a.slots) hi = mid; else lo = mid;
-        }
-      }
-      most = hi;
-    }
-    bool found = false;
-#pragma unroll
-    for (int c = 0; c < kSets; ++c) {
-      if (found || c * 64 >= a.seqs) continue;
-      const int per = parts_of(a, lq[c], steps[c], most), upto = wave_prefix(n[c] * per);
-      const int here = __builtin_amdgcn_readlane(upto, 63);
-      if (u < here) {
-        const int j = __builtin_ctzll(__ballot(upto > u));
-        pc->seq = c * 64 + j;
-        pc->q0 = __builtin_amdgcn_readlane(q0[c], j);
-        pc->lq = __builtin_amdgcn_readlane(lq[c], j);
-        pc->len = __builtin_amdgcn_readlane(len[c], j);
-        tiles = __builtin_amdgcn_readlane(n[c], j);
-        parts = __builtin_amdgcn_readlane(per, j);
-        u -= __builtin_amdgcn_readlane(upto, j) - tiles * parts;
-        found = true;
-      } else {
-        u -= here;
-      }
-    }
-    if (!found) return false;
-    tile = tiles - 1 - u / parts;
-    part = u % parts;
+  float total = 0.0f, longest = 0.0f, pieces = 0.0f;
+  for (int s0 = 0; s0 < a.seqs; s0 += 64) {
+    const Seq q = s0 == 0 ? first : Seq(a, s0 + lane);
+    const float cost = float(q.steps()) * q.tile_cost(a), n = float(q.tiles(a)) / float(q.heads(a));
+    longest = fmaxf(longest, cost);
+    pieces += n;
+    // (under a causal mask the mean tile sees half a chunk less than the last one)
+    total += n * (a.causal ? fmaxf(cost - float(q.lq) * (0.5f / kTileKeys), 0.5f * cost) : cost);
   }
-  pc->row0 = tile * kTileRows;
+  total = wave_sum_f(total);
+  pieces = wave_sum_f(pieces);
+  if (pieces + 2.0f >= float(a.slots)) return 1e9f;
+  longest = max_over_wave(longest);
+  const float share = total * __builtin_amdgcn_rcpf(a.resident);
+  const float limit = lane == 63 ? 1e9f : share * 0.75f * __builtin_amdgcn_exp2f(float(lane) * 0.035624f);
+  // the four waves take every fourth sequence each
+  float sum = 0.0f, split = 0.0f, top = 0.0f;  // pieces, those that are parts, the longest one's time
+  for (int s0 = 0; s0 < a.seqs; s0 += 64) {
+    const Seq q = s0 == 0 ? first : Seq(a, s0 + lane);
+    const int cap = q.cap(a);
+    const float cost = float(q.steps()) * q.tile_cost(a), n = float(q.tiles(a)) / float(q.heads(a));
+    for (int j = threadIdx.x >> 6; j < min(a.seqs - s0, 64); j += 4) {
+      auto of = [&](float x) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), j)); };
+      const float sc = of(cost), sn = of(n);
+      const float p = parts_of(sc, __builtin_amdgcn_readlane(cap, j), limit);
+      sum += sn * p;
+      split += p > 1.0f ? sn * p : 0.0f;
+      top = fmaxf(top, sn > 0.0f ? sc * __builtin_amdgcn_rcpf(p) : 0.0f);
+    }
+  }
+  float4* const each = reinterpret_cast<float4*>(lds);
+  each[threadIdx.x] = make_float4(sum, split, top, 0.0f);
+  __syncthreads();
+  sum = split = top = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float4 x = each[w * 64 + lane];
+    sum += x.x;
+    split += x.y;
+    top = fmaxf(top, x.z);
+  }
+  __syncthreads();
+  // Pieces that run at once take the longest one's time, alone on a compute unit less; more pieces
+  // share the time of all, and wait for half a last one.  Each piece takes kPieceCost to start, and
+  // its sums' way through memory where it is a part.
+  float time = sum <= a.resident ? (sum <= 0.5f * a.resident ? kAloneCost : 1.0f) * top + kPieceCost
+                                 : (total + kPieceCost * sum) * __builtin_amdgcn_rcpf(a.resident) + 0.5f * top;
+  time += kJoinCost * float(a.hkv) * split;
+  if (sum + 2.0f > float(a.slots)) time = 1e30f;
+  const float best = -max_over_wave(-time);
+  const uint64_t where = __ballot(time == best);
+  return best < 1e30f && where ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(limit), __builtin_ctzll(where)))
+                               : 1e9f;
+}
+
+// Piece `u` of those of KV head `kvh`, or false.  Pieces for several heads are dealt out to those heads'
+// lists in turn.  Pieces of long time come first.  `used`: the slots that all parts take.  All threads
+// call it; lds: 4 KB.
+__device__ __forceinline__ bool find_piece(const ChunkArgs& a, int kvh, int u, uint8_t* lds, Piece* pc,
+                                           int* used) {
+  const int lane = threadIdx.x & 63;
+  const Seq first(a, lane);
+  const float most = a.slots > 0 ? find_limit(a, first, lds) : 1e9f;
+  bool found = false;
+  int before = 0;
+  *used = 0;
+  for (int order = 0; order < 2; ++order) {
+    int dealt2 = 0, dealt4 = 0, slots = 0;  // of the sequences so far
+    for (int s0 = 0; s0 < a.seqs; s0 += 64) {
+      const Seq q = s0 == 0 ? first : Seq(a, s0 + lane);
+      const int n = q.tiles(a), heads = q.heads(a), shift = heads >> 1;
+      const float cost = float(q.steps()) * q.tile_cost(a);
+      const float fp = a.slots > 0 ? parts_of(cost, q.cap(a), most) : 1.0f;
+      const int p = int(fp);
+      // the parts of this sequence that fall to this head's list, and the first of them
+      const int all = heads > 1 && n > 0 ? p : 0;
+      const int upto2 = wave_prefix(heads == 2 ? all : 0), upto4 = wave_prefix(heads == 4 ? all : 0);
+      const int base = heads == 2 ? dealt2 + upto2 - all : dealt4 + upto4 - all;
+      dealt2 += last_lane(upto2);
+      dealt4 += last_lane(upto4);
+      const int r = kvh & (heads - 1), skip = heads - 1 - r;
+      const int deal = ((base + all + skip) >> shift) - ((base + skip) >> shift);
+      const int p0 = (r - base) & (heads - 1);
+      const int own_slots = p == 1 || n == 0 ? 0 : heads > 1 ? p * (a.hkv >> shift) : n * p * a.hkv;
+      const int slots_upto = wave_prefix(own_slots);
+      const bool is_long = cost > 0.5f * most * fp;
+      const int mine = is_long == (order == 0) ? heads > 1 ? deal : n * p : 0;
+      const int upto = wave_prefix(mine), here = last_lane(upto);
+      if (!found && u < before + here) {
+        const int j = __builtin_ctzll(__ballot(upto > u - before));
+        auto of = [&](int x) { return __builtin_amdgcn_readlane(x, j); };
+        const int i = u - before - (of(upto) - of(mine));
+        pc->seq = s0 + j;
+        pc->q0 = of(q.q0);
+        pc->lq = of(q.lq);
+        pc->len = of(q.len);
+        pc->parts = of(p);
+        pc->heads = of(heads);
+        int tile = 0;
+        if (pc->heads > 1) {
+          pc->part = of(p0) + i * pc->heads;
+          pc->kvh = kvh & ~(pc->heads - 1);
+        } else {
+          tile = of(n) - 1 - i / pc->parts;
+          pc->part = i % pc->parts;
+          pc->kvh = kvh;
+        }
+        pc->row0 = tile * kTileRows;
+        pc->slot = slots + of(slots_upto) - of(own_slots) +
+                   (pc->heads > 1 ? (pc->kvh >> (pc->heads >> 1)) : tile * a.hkv + pc->kvh) * pc->parts + pc->part;
+        found = true;
+      }
+      before += here;
+      slots += last_lane(slots_upto);
+    }
+    *used = slots;
+    if (found) break;
+  }
+  if (!found) return false;
   pc->rows = min(pc->lq * a.group - pc->row0, kTileRows);
   const int last = int(a.by_group.div(pc->row0 + pc->rows - 1));
-  const int steps = key_tiles(pc->seen(a, last));
-  parts = max(min(parts, steps / kMinPart), 1);  // an early tile of a prompt sees less
-  if (part >= parts) return false;
-  pc->part = part;
-  pc->parts = parts;
-  pc->from = int(int64_t(steps) * part / parts);
-  pc->to = int(int64_t(steps) * (part + 1) / parts);
+  const int steps = (pc->seen(a, last) + kTileKeys - 1) / kTileKeys;
+  // (an early tile of a prompt sees less: some of its parts may be empty)
+  pc->from = int(int64_t(steps) * pc->part / pc->parts);
+  pc->to = int(int64_t(steps) * (pc->part + 1) / pc->parts);
   return true;
 }
 
@@ -332,20 +398,24 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
     return __builtin_amdgcn_readfirstlane(all) != 0;
   };
   Piece pc;
-  const bool any = find_piece(a, u, &pc);
-  const int64_t slot = int64_t(kvh) * a.slots + u;
-  if (u < a.slots && tid == 0)
-    a.pieces[slot] = any ? make_int4(pc.q0, pc.row0, pc.rows, pc.part | pc.parts << 16)
-                         : make_int4(0, 0, 0, 0);
+  int used;
+  const bool any = find_piece(a, kvh, u, t3, &pc, &used);
+  if (a.slots > 0 && blockIdx.x == 0 && tid == 0) a.parts[a.slots * a.hkv] = make_int4(used, 0, 0, 0);
   if (!any) return;
 
-  Work<D> wk{a, pc, kvh, a.tables + pc.seq * a.ts, false};
-  // Few rows: the waves take different positions instead of different rows.
-  const bool few = pc.rows <= kFewRows;
-  const int row_waves = !few ? 4 : pc.rows > 32 ? 2 : 1, key_waves = 4 / row_waves;
+  // Few rows: the waves take different KV heads, and different positions, instead of different rows.
+  const bool few = pc.lq * a.group <= kFewRows;
+  const int row_waves = !few ? 4 : pc.rows > kWaveRows ? 2 : 1, width = row_waves * pc.heads;
+  const int key_waves = 4 / width, key_wave = wave / width;
+  const int head_wave = (wave & (width - 1)) / row_waves;
   const int mine = (wave & (row_waves - 1)) * kWaveRows;   // this wave's first row of the tile
-  const int key_wave = wave / row_waves;
   const int row = mine + col;                              // this lane's
+  const int slot_row = head_wave * row_waves * kWaveRows + row;
+  kvh = pc.kvh + head_wave;
+  if (pc.parts > 1 && tid == 0)
+    a.parts[pc.slot] = make_int4(pc.q0, pc.row0, pc.rows | row_waves << 8 | pc.heads << 12 | pc.kvh << 16,
+                                 pc.part | pc.parts << 16);
+  Work<D> wk{a, pc, kvh, a.tables + pc.seq * a.ts, false};
   auto query_of = [&](int r) { return int(a.by_group.div(pc.row0 + r)); };
   const int my_row = min(row, pc.rows - 1), my_query = query_of(my_row);
   const int my_head = kvh * a.group + pc.row0 + my_row - my_query * a.group;
@@ -548,7 +618,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
   float4* const s_stats = reinterpret_cast<float4*>(t2);
   for (int n = key_waves / 2; n >= 1; n /= 2) {
     __syncthreads();
-    const int to = wave & (row_waves * n - 1);
+    const int to = wave & (width * n - 1);
     float* const s_o = reinterpret_cast<float*>(to == 0 ? t0 : t1);
     if (key_wave >= n && key_wave < 2 * n) {
 #pragma unroll
@@ -582,7 +652,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
   }
   if (key_wave > 0 || row >= pc.rows) return;
   if (pc.parts > 1) {
-    const int64_t to = slot * kTileRows + row;
+    const int64_t to = int64_t(pc.slot) * kTileRows + slot_row;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -605,39 +675,70 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
                      cvt_bf16x2(o[i][r + 2] * inv, o[i][r + 3] * inv));
 }
 
-// Adds up the parts of a tile in order: the workgroups of each part take a share of its rows, D/4
-// lanes a row.
+// Adds up the parts of a piece in order.  The workgroups of each part take a share of its rows, D/4 lanes
+// a row: each such group of lanes a row of its own, or, of many parts, every kGroups-th part of the
+// workgroup's row.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinGroups = 4;  // workgroups of a part
+constexpr int kJoinGroups = 8;   // workgroups of a part
+constexpr int kManyParts = 16;
 template <int D>
 __global__ __launch_bounds__(kJoinThreads) void chunk_join_kernel(const ChunkArgs a) {
-  constexpr int kLanes = D / 4, kRows = kJoinThreads / kLanes;
-  const int slot = blockIdx.x / kJoinGroups, kvh = slot / a.slots;
-  const int4 p = a.pieces[slot];
-  const int part = p.w & 0xFFFF, parts = p.w >> 16;
-  if (parts <= 1) return;
+  constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
+  const int slot = blockIdx.x / kJoinGroups;
+  if (slot >= a.parts[a.slots * a.hkv].x) return;
+  const int4 x = a.parts[slot];
+  const int part = x.w & 0xFFFF, parts = x.w >> 16;
+  const int rows = x.z & 0xFF, row_waves = x.z >> 8 & 0xF, heads = x.z >> 12 & 0xF, kvh = int(uint32_t(x.z) >> 16);
   const int share = part * kJoinGroups + blockIdx.x % kJoinGroups, shares = parts * kJoinGroups;
-  const int d = threadIdx.x % kLanes * 4;
-  const int64_t first = int64_t(slot - part) * kTileRows;  // an item's parts lie side by side
-  for (int r = p.z * share / shares + int(threadIdx.x) / kLanes; r < p.z * (share + 1) / shares; r += kRows) {
+  const int group = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
+  const int64_t first = int64_t(slot - part) * kTileRows;  // a piece's parts lie side by side
+  const bool many = parts > kManyParts;
+  __shared__ __attribute__((aligned(16))) float4 s_v[kGroups][kLanes];
+  __shared__ __attribute__((aligned(16))) float4 s_st[kGroups];
+  const int step = many ? shares : shares * kGroups;
+  for (int i = many ? share : share * kGroups + group; i - (many ? 0 : group) < heads * rows; i += step) {
+    const bool live = i < heads * rows;
+    const int h = live ? i / rows : 0, r = live ? i - h * rows : 0;
     float ref = neg_inf(), total = 0.0f, rounded = 0.0f;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-      const int64_t at = first + int64_t(i) * kTileRows + r;
-      const float4 x = *reinterpret_cast<const float4*>(a.sums + at * D + d);
-      const float4 st = a.stats[at];
+    auto add = [&](float4 st, float4 x) {
       const float to = fmaxf(ref, st.x);
       const float f = ref == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(ref - to);
-      const float h = st.x == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(st.x - to);
+      const float g = st.x == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(st.x - to);
       ref = to;
-      total = total * f + st.y * h;
-      rounded = rounded * f + st.z * h;
-      v.x = v.x * f + x.x * h; v.y = v.y * f + x.y * h;
-      v.z = v.z * f + x.z * h; v.w = v.w * f + x.w * h;
+      total = total * f + st.y * g;
+      rounded = rounded * f + st.z * g;
+      v.x = v.x * f + x.x * g; v.y = v.y * f + x.y * g;
+      v.z = v.z * f + x.z * g; v.w = v.w * f + x.w * g;
+    };
+    const int64_t at0 = first + h * row_waves * kWaveRows + r;
+    if (live) {
+      const int by = many ? kGroups : 1;
+      for (int p = many ? group : 0; p < parts; p += 4 * by) {
+        float4 y[4], st[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int64_t at = at0 + int64_t(min(p + k * by, parts - 1)) * kTileRows;
+          y[k] = *reinterpret_cast<const float4*>(a.sums + at * D + d);
+          st[k] = a.stats[at];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (p + k * by < parts) add(st[k], y[k]);
+      }
     }
-    const int q = int(a.by_group.div(p.y + r)), head = kvh * a.group + p.y + r - q * a.group;
-    const int64_t q_row = p.x + q;
+    if (many) {
+      s_v[group][threadIdx.x % kLanes] = v;
+      if (d == 0) s_st[group] = make_float4(ref, total, rounded, 0.0f);
+      __syncthreads();
+      if (group == 0)
+        for (int g = 1; g < kGroups; ++g) add(s_st[g], s_v[g][threadIdx.x]);
+      __syncthreads();
+      if (group > 0) continue;
+    }
+    if (!live) continue;
+    const int q = int(a.by_group.div(x.y + r)), head = (kvh + h) * a.group + x.y + r - q * a.group;
+    const int64_t q_row = x.x + q;
     const float inv = total == 0.0f ? 0.0f : a.v_scale / rounded;
     *reinterpret_cast<uint2*>(a.out + q_row * a.os + int64_t(head) * D + d) =
         make_uint2(cvt_bf16x2(v.x * inv, v.y * inv), cvt_bf16x2(v.z * inv, v.w * inv));
@@ -656,6 +757,7 @@ int chunk_shape(int32_t seqs, int32_t tq, int32_t hq, int32_t hkv, int32_t d) {
 
 struct ChunkPlan {
   int slots;       // pieces of a KV head when sequences are split; 0: they are not
+  float resident;  // pieces of a KV head that run at once
   int64_t pieces;  // that a KV head may have
   uint64_t sums_bytes, stats_bytes, bytes;
 };
@@ -663,16 +765,16 @@ ChunkPlan chunk_plan(int32_t seqs, int32_t tq, int32_t hq, int32_t hkv, int32_t 
   ChunkPlan p = {};
   const int64_t rows = int64_t(tq) * (hq / hkv);
   const int64_t some = seqs < tq ? seqs : tq;  // sequences that have a query
-  p.pieces = (rows + some * (kTileRows - 1)) / kTileRows;
-  const int at_once = num_cus() * (d == 256 ? 1 : d == 128 ? 2 : 3);
-  const int slots = at_once / hkv;
+  p.pieces = (rows + some * (kTileRows - 1)) / kTileRows + 2;  // (lists that are dealt to: one more each)
+  p.resident = float(num_cus() * (d == 256 ? 1 : d == 128 ? 2 : 3)) / float(hkv);
+  const int slots = int(1.75f * p.resident);
   // (with whole tiles for all slots nothing is split)
-  if (seqs <= kSplitSeqs && slots > 1 && rows / kTileRows < slots) p.slots = slots;
+  if (seqs <= kSplitSeqs && slots > 3 && rows / kTileRows < slots) p.slots = slots;
   if (p.slots > p.pieces) p.pieces = p.slots;
   const uint64_t all = uint64_t(p.slots) * hkv * kTileRows;
   p.sums_bytes = all * d * 4;
   p.stats_bytes = all * 16;
-  p.bytes = p.sums_bytes + p.stats_bytes + uint64_t(p.slots) * hkv * 16;
+  p.bytes = p.sums_bytes + p.stats_bytes + (uint64_t(p.slots) * hkv + 1) * 16;
   return p;
 }
 
@@ -738,13 +840,14 @@ extern "C" int fp8_attn_chunk(const uint16_t* q, const uint8_t* k_cache, const u
   if (p.slots > 0) {
     a.sums = reinterpret_cast<float*>(ws);
     a.stats = reinterpret_cast<float4*>(ws + p.sums_bytes);
-    a.pieces = reinterpret_cast<int4*>(ws + p.sums_bytes + p.stats_bytes);
+    a.parts = reinterpret_cast<int4*>(ws + p.sums_bytes + p.stats_bytes);
   }
   a.ts = table_stride, a.qs = q_stride, a.os = out_stride, a.cs = cache_stride, a.nblocks = num_blocks;
   a.seqs = num_seqs, a.width = max_blocks, a.tq = total_q, a.hq = num_q_heads, a.hkv = num_kv_heads;
   a.group = num_q_heads / num_kv_heads, a.bs = block_size, a.causal = causal != 0;
   a.by_group = FastDiv(uint32_t(a.group)), a.by_block = FastDiv(uint32_t(block_size));
-  a.slots = p.slots, a.scale_log2 = softmax_scale * k_scale * kLog2e, a.v_scale = v_scale;
+  a.most_heads = num_kv_heads % 4 == 0 ? 4 : num_kv_heads % 2 == 0 ? 2 : 1;
+  a.slots = p.slots, a.resident = p.resident, a.scale_log2 = softmax_scale * k_scale * kLog2e, a.v_scale = v_scale;
   const int64_t per = num_kv_heads % 8 == 0 ? 8 : 8 % num_kv_heads == 0 ? 8 / num_kv_heads : 1;
   const int64_t blocks = num_kv_heads % 8 == 0 ? p.pieces * num_kv_heads
                                                : (p.pieces + per - 1) / per * per * num_kv_heads;
