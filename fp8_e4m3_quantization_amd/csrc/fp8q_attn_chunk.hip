@@ -24,7 +24,7 @@ constexpr int kThreads = 256;
 constexpr int kSplitSeqs = 256;  // batches of more sequences are not split along the positions
 constexpr int kFewRows = 64;     // so many rows of a sequence and KV head at most: another form
 constexpr int kMinPart = 4;      // tiles of positions of a part, at least
-constexpr int kMinFewPart = 2;   // the same of few rows
+constexpr int kMinFewPart = 1;   // the same of few rows
 // Times, in that of a tile of positions of a workgroup of many rows that shares its compute unit:
 constexpr float kFewCost = 0.6f;    // a tile of positions of few rows, for each KV head
 constexpr float kAloneCost = 0.6f;  // a tile of a workgroup alone on its compute unit
@@ -49,6 +49,15 @@ struct ChunkArgs {
   float resident;  // pieces of a KV head that run at once
   float scale_log2, v_scale;
 };
+
+// The kernel's arguments, read again from where the launch left them: scalars that a loop does not need
+// take no registers from it.
+__device__ __forceinline__ const ChunkArgs& own_args() {
+  typedef const __attribute__((address_space(4))) ChunkArgs* Kernarg;
+  Kernarg p = (Kernarg)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const ChunkArgs*)p;
+}
 
 // A sequence, whatever the lists hold: its first query row, queries and positions; and how its rows
 // of a KV head are worked on.
@@ -82,15 +91,33 @@ struct Seq {
   }
 };
 
+template <int kCtrl, int kRowMask>
+__device__ __forceinline__ float row_step(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, kRowMask, 0xF, false));
+}
+
 // Parts, `cap` at most, of a sequence whose pieces take `cost` when one takes at most about `most`.  The
 // same arithmetic in every workgroup: all agree.
 __device__ __forceinline__ float parts_of(float cost, int cap, float most) {
   return fmaxf(fminf(__builtin_ceilf(cost * __builtin_amdgcn_rcpf(most)), float(cap)), 1.0f);
 }
 
-__device__ __forceinline__ float wave_sum_f(float v) {
-  for (int m = 1; m < 64; m *= 2) v += __shfl_xor(v, m);
-  return v;
+// Sums, and largest of values that are not negative, over the wave.
+template <typename Op>
+__device__ __forceinline__ float wave_reduce(float v, Op op) {
+  v = op(v, row_step<0x111, 0xF>(v));  // row_shr:1
+  v = op(v, row_step<0x112, 0xF>(v));
+  v = op(v, row_step<0x114, 0xF>(v));
+  v = op(v, row_step<0x118, 0xF>(v));
+  v = op(v, row_step<0x142, 0xA>(v));  // row_bcast:15 into rows 1 and 3
+  v = op(v, row_step<0x143, 0xC>(v));  // row_bcast:31 into rows 2 and 3
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  return wave_reduce(v, [](float x, float y) { return x + y; });
+}
+__device__ __forceinline__ float wave_max(float v) {
+  return wave_reduce(v, [](float x, float y) { return fmaxf(x, y); });
 }
 __device__ __forceinline__ int last_lane(int v) { return __builtin_amdgcn_readlane(v, 63); }
 
@@ -113,28 +140,27 @@ struct Piece {
 // 2.5 %; the least estimated time wins.  All threads call it; lds: 4 KB.
 __device__ __forceinline__ float find_limit(const ChunkArgs& a, const Seq& first, uint8_t* lds) {
   const int lane = threadIdx.x & 63;
-  float total = 0.0f, longest = 0.0f, pieces = 0.0f;
+  float total = 0.0f, pieces = 0.0f;
   for (int s0 = 0; s0 < a.seqs; s0 += 64) {
     const Seq q = s0 == 0 ? first : Seq(a, s0 + lane);
-    const float cost = float(q.steps()) * q.tile_cost(a), n = float(q.tiles(a)) / float(q.heads(a));
-    longest = fmaxf(longest, cost);
+    const float cost = float(q.steps()) * q.tile_cost(a), n = float(q.tiles(a)) * (1.0f / float(q.heads(a)));
     pieces += n;
     // (under a causal mask the mean tile sees half a chunk less than the last one)
     total += n * (a.causal ? fmaxf(cost - float(q.lq) * (0.5f / kTileKeys), 0.5f * cost) : cost);
   }
-  total = wave_sum_f(total);
-  pieces = wave_sum_f(pieces);
+  total = wave_sum(total);
+  pieces = wave_sum(pieces);
   if (pieces + 2.0f >= float(a.slots)) return 1e9f;
-  longest = max_over_wave(longest);
   const float share = total * __builtin_amdgcn_rcpf(a.resident);
   const float limit = lane == 63 ? 1e9f : share * 0.75f * __builtin_amdgcn_exp2f(float(lane) * 0.035624f);
-  // the four waves take every fourth sequence each
+  // (of many sequences the four waves take every fourth each)
+  const bool shared = a.seqs > 8;
   float sum = 0.0f, split = 0.0f, top = 0.0f;  // pieces, those that are parts, the longest one's time
   for (int s0 = 0; s0 < a.seqs; s0 += 64) {
     const Seq q = s0 == 0 ? first : Seq(a, s0 + lane);
     const int cap = q.cap(a);
-    const float cost = float(q.steps()) * q.tile_cost(a), n = float(q.tiles(a)) / float(q.heads(a));
-    for (int j = threadIdx.x >> 6; j < min(a.seqs - s0, 64); j += 4) {
+    const float cost = float(q.steps()) * q.tile_cost(a), n = float(q.tiles(a)) * (1.0f / float(q.heads(a)));
+    for (int j = shared ? threadIdx.x >> 6 : 0; j < min(a.seqs - s0, 64); j += shared ? 4 : 1) {
       auto of = [&](float x) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), j)); };
       const float sc = of(cost), sn = of(n);
       const float p = parts_of(sc, __builtin_amdgcn_readlane(cap, j), limit);
@@ -143,18 +169,20 @@ __device__ __forceinline__ float find_limit(const ChunkArgs& a, const Seq& first
       top = fmaxf(top, sn > 0.0f ? sc * __builtin_amdgcn_rcpf(p) : 0.0f);
     }
   }
-  float4* const each = reinterpret_cast<float4*>(lds);
-  each[threadIdx.x] = make_float4(sum, split, top, 0.0f);
-  __syncthreads();
-  sum = split = top = 0.0f;
+  if (shared) {
+    float4* const each = reinterpret_cast<float4*>(lds);
+    each[threadIdx.x] = make_float4(sum, split, top, 0.0f);
+    __syncthreads();
+    sum = split = top = 0.0f;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float4 x = each[w * 64 + lane];
-    sum += x.x;
-    split += x.y;
-    top = fmaxf(top, x.z);
+    for (int w = 0; w < 4; ++w) {
+      const float4 x = each[w * 64 + lane];
+      sum += x.x;
+      split += x.y;
+      top = fmaxf(top, x.z);
+    }
+    __syncthreads();
   }
-  __syncthreads();
   // Pieces that run at once take the longest one's time, alone on a compute unit less; more pieces
   // share the time of all, and wait for half a last one.  Each piece takes kPieceCost to start, and
   // its sums' way through memory where it is a part.
@@ -162,10 +190,10 @@ __device__ __forceinline__ float find_limit(const ChunkArgs& a, const Seq& first
                                  : (total + kPieceCost * sum) * __builtin_amdgcn_rcpf(a.resident) + 0.5f * top;
   time += kJoinCost * float(a.hkv) * split;
   if (sum + 2.0f > float(a.slots)) time = 1e30f;
-  const float best = -max_over_wave(-time);
-  const uint64_t where = __ballot(time == best);
-  return best < 1e30f && where ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(limit), __builtin_ctzll(where)))
-                               : 1e9f;
+  // the least time, as the largest difference of the bits from an upper end's
+  const float key = __uint_as_float(0x7F000000u - __float_as_uint(time));
+  const uint64_t where = __ballot(key == wave_max(key) && time < 1e30f);
+  return where ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(limit), __builtin_ctzll(where))) : 1e9f;
 }
 
 // Piece `u` of those of KV head `kvh`, or false.  Pieces for several heads are dealt out to those heads'
@@ -244,15 +272,13 @@ __device__ __forceinline__ bool find_piece(const ChunkArgs& a, int kvh, int u, u
 // What the kernel's two forms share: a piece, and the lane's place in it.
 template <int D>
 struct Work {
-  const ChunkArgs& a;
   Piece pc;
   int kvh;
-  const int32_t* table;
   bool any_bad;    // some position of the piece lies in a block that does not exist
 
-  // The id of a position's block (behind the last position: the last one's).
-  __device__ __forceinline__ int block_at(int pos) const {
-    return table[a.by_block.div(min(pos, pc.len - 1))];
+  // A position's block (behind the last position: the last one's).
+  __device__ __forceinline__ int block_at(const ChunkArgs& a, int pos) const {
+    return a.tables[pc.seq * a.ts + a.by_block.div(min(pos, pc.len - 1))];
   }
   // Scores of positions that a row does not see, or that lie in blocks that do not exist, are
   // -infinity; s holds positions p0 .. p0 + 32 kBlocks - 1.
@@ -267,18 +293,25 @@ struct Work {
         if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // few conditions alive at a time
       }
     if (any_bad) {  // rare
+      const ChunkArgs& a = own_args();
+      uint32_t good = 0;
+#pragma unroll 1
+      for (int i = 0; i < 16 * kBlocks; ++i) {
+        const int pos = p0 + 32 * (i >> 4) + 8 * (i >> 2 & 3) + (i & 3) + 4 * half;
+        good |= uint32_t(uint32_t(block_at(a, pos)) < a.nblocks) << i;
+      }
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          s[b][r] = uint32_t(block_at(p0 + 32 * b + 8 * (r >> 2) + (r & 3) + 4 * half)) < a.nblocks ? s[b][r] : neg_inf();
+        for (int r = 0; r < 16; ++r) s[b][r] = good >> (16 * b + r) & 1 ? s[b][r] : neg_inf();
     }
   }
   // NaN codes that were left out of positions from `first` on reach a row that sees them.
   __device__ __forceinline__ void take_nans(RowSums<D>& sums, int first, int limit) const {
+    const ChunkArgs& a = own_args();
     const int half = (threadIdx.x & 63) >> 5, end = min(limit, min(pc.to * kTileKeys, pc.len));
     for (int pos = first; pos < end; ++pos) {
-      const int id = block_at(pos);
+      const int id = block_at(a, pos);
       if (uint32_t(id) >= a.nblocks) continue;
       const int off = pos - int(a.by_block.div(pos)) * a.bs;
       const uint8_t* v = a.vc + id * a.cs + off * (int64_t(a.hkv) * D) + int64_t(kvh) * D + 4 * half;
@@ -328,10 +361,14 @@ struct Rows {
       off[j] -= over ? a.bs : 0;
     }
   }
-  // A block that does not exist is replaced by the first one: what is read there does not count.
-  __device__ __forceinline__ int64_t place(const ChunkArgs& a, int j) const {
-    const uint32_t good = uint32_t(id[j]) < a.nblocks ? id[j] : 0;
-    return int64_t(uint64_t(good) * uint32_t(a.cs) + uint64_t(uint32_t(at[j])) * uint32_t(a.hkv * D));
+  // Where the rows that are copied next lie.  A block that does not exist is replaced by the first
+  // one: what is read there does not count.
+  __device__ __forceinline__ void places(const ChunkArgs& a, int64_t* to) const {
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const uint32_t good = uint32_t(id[j]) < a.nblocks ? id[j] : 0;
+      to[j] = int64_t(uint64_t(good) * uint32_t(a.cs) + uint64_t(uint32_t(at[j])) * uint32_t(a.hkv * D));
+    }
   }
 };
 
@@ -343,32 +380,26 @@ __device__ __forceinline__ void copy16(const uint8_t* from, uint8_t* to) {
 // s_waitcnt's operand for vmcnt(n).
 constexpr int until_vmcnt(int n) { return (n & 15) | (n >> 4) << 14 | 0x0F70; }
 
-// The order of a turn: the score products with the weights and the widening of the keys between them,
-// then the value products with the widening of the values.
-template <int D>
-__device__ __forceinline__ void pair_up() {
-  constexpr int kMfma = 0x008, kVector = 0x002, kLdsRead = 0x100;
-  __builtin_amdgcn_sched_group_barrier(kLdsRead, 4, 0);
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
-    __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(kVector, 10, 0);
-    __builtin_amdgcn_sched_group_barrier(kLdsRead, 1, 0);
-  }
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
-    __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(kLdsRead, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(kVector, 8, 0);
+// The order of a step of a turn: the LDS reads of the next one, then products with vector instructions
+// between them.
+template <int kReads, int kProducts, int kVectors>
+__device__ __forceinline__ void in_order() {
+  __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
+  if constexpr (kProducts > 0) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, kVectors, 0);
+    in_order<0, kProducts - 1, kVectors>();
   }
 }
 
 template <int D>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chunk_kernel(const ChunkArgs a) {
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chunk_kernel(const ChunkArgs) {
+  const ChunkArgs& a = own_args();
   // Four tiles of codes, keys then values
   constexpr int kTileBytes = kTileKeys * D;
   __shared__ __attribute__((aligned(16))) uint8_t t0[2 * kTileBytes], t1[2 * kTileBytes];
   __shared__ __attribute__((aligned(16))) uint8_t t2[2 * kTileBytes], t3[2 * kTileBytes];
+  __shared__ int s_flags[2][4];
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
@@ -387,15 +418,13 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
       u = blockIdx.x / a.hkv;
     }
   }
-  // Whether `x` holds in any lane of any wave; LDS is free before and after.
-  auto any_of_all = [&](bool x) {
-    int* const flags = reinterpret_cast<int*>(t3);
-    const bool mine_any = __any(x);
-    if (lane == 0) flags[wave] = mine_any;
-    __syncthreads();
-    const int all = flags[0] | flags[1] | flags[2] | flags[3];
-    __syncthreads();
-    return __builtin_amdgcn_readfirstlane(all) != 0;
+  // Whether `x` holds in any lane of any wave, at the next barrier.
+  auto tell = [&](int i, bool x) {
+    const bool mine = __any(x);
+    if (lane == 0) s_flags[i][wave] = mine;
+  };
+  auto told = [&](int i) {
+    return __builtin_amdgcn_readfirstlane(s_flags[i][0] | s_flags[i][1] | s_flags[i][2] | s_flags[i][3]) != 0;
   };
   Piece pc;
   int used;
@@ -415,7 +444,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
   if (pc.parts > 1 && tid == 0)
     a.parts[pc.slot] = make_int4(pc.q0, pc.row0, pc.rows | row_waves << 8 | pc.heads << 12 | pc.kvh << 16,
                                  pc.part | pc.parts << 16);
-  Work<D> wk{a, pc, kvh, a.tables + pc.seq * a.ts, false};
+  Work<D> wk{pc, kvh, false};
   auto query_of = [&](int r) { return int(a.by_group.div(pc.row0 + r)); };
   const int my_row = min(row, pc.rows - 1), my_query = query_of(my_row);
   const int my_head = kvh * a.group + pc.row0 + my_row - my_query * a.group;
@@ -432,13 +461,19 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
       qf[s] = __builtin_bit_cast(v8bf, *reinterpret_cast<const uint4*>(src + 32 * (s >> 1) + 8 * (s & 1)));
   }
   const int last_block = int(a.by_block.div(max(pc.len - 1, 0)));
-  {
-    bool bad = false;
-    const int first = a.by_block.div(pc.from * kTileKeys);
-    const int last = pc.from < pc.to ? int(a.by_block.div(min(pc.to * kTileKeys, pc.len) - 1)) : first - 1;
-    for (int i = first + tid; i <= last; i += kThreads) bad |= uint32_t(wk.table[i]) >= a.nblocks;
-    wk.any_bad = any_of_all(bad);
-  }
+  // Whether all blocks exist, which the table tells beside the first copies: a first number of each
+  // thread's is read before those.
+  const int first_block = int(a.by_block.div(pc.from * kTileKeys)) + tid;
+  const int end_block = pc.from < pc.to ? int(a.by_block.div(min(pc.to * kTileKeys, pc.len) - 1)) + 1 : 0;
+  const int32_t* const table = a.tables + pc.seq * a.ts;
+  const int one_id = first_block < end_block ? table[first_block] : 0;
+  auto look_for_bad = [&]() {
+    bool bad = uint32_t(one_id) >= a.nblocks;
+    for (int i = first_block + kThreads; i < end_block; i += kThreads) bad |= uint32_t(table[i]) >= a.nblocks;
+    tell(0, bad);
+    __syncthreads();
+    wk.any_bad = told(0);
+  };
 
   RowSums<D> sums;
   sums.clear();
@@ -448,9 +483,10 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
   const uint8_t* const kc = a.kc + int64_t(kvh) * D;
   const uint8_t* const vc = a.vc + int64_t(kvh) * D;
 
-  if (few) {
+  if (row_waves == 1) {
     // Each wave takes every key_waves-th block of 32 positions, two blocks ahead in LDS.
     const int lane = own_lane();
+    const ChunkArgs& a = own_args();
     constexpr int kCopies = D / 32;                        // copies of a block's keys, or values
     typedef Rows<D, kCopies> R;
     const int f_row = lane / R::kLanes, f_place = lane % R::kLanes;
@@ -459,17 +495,20 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
     R rows;
     // Copies of the next block, after the block numbers of the one behind it: what waits for those
     // need not wait for the copies.
-    auto copy_block = [&](uint8_t* ks, uint8_t* vs) {
-      int64_t at[kCopies];
-#pragma unroll
-      for (int j = 0; j < kCopies; ++j) at[j] = rows.place(a, j);
-      rows.read_ids(a, wk.table, last_block);
+    auto copy_at = [&](const int64_t* at, uint8_t* ks, uint8_t* vs) {
 #pragma unroll
       for (int j = 0; j < kCopies; ++j) {
         const int r = j * R::kAtOnce + f_row;
         copy16(kc + at[j] + (f_place ^ key_turn<D>(r)) * 16, ks + j * 1024);
         copy16(vc + at[j] + (f_place ^ value_turn<D>(r)) * 16, vs + j * 1024);
       }
+    };
+    auto copy_block = [&](uint8_t* ks, uint8_t* vs) {
+      int64_t at[kCopies];
+      rows.places(a, at);
+      rows.read_ids(a, table, last_block);
+      asm volatile("" ::: "memory");
+      copy_at(at, ks, vs);
     };
     // Block n; with kEdge it may be seen in part.
     auto block = [&](const uint8_t* ks, const uint8_t* vs, auto edge, int lane) {
@@ -497,14 +536,25 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
       }
       n += key_waves;
     };
+    const int mine32 = wave * 32 * D;
     if (n < end) {
-      const int mine32 = wave * 32 * D;
+      rows.start(a, 32 * n + f_row, R::kAtOnce, 32 * key_waves);
+      // (the first blocks' block numbers are read all at once)
+      rows.read_ids(a, table, last_block);
+      R next = rows;
+      next.read_ids(a, table, last_block);
+      int64_t at[2][kCopies];
+      rows.places(a, at[0]);
+      next.places(a, at[1]);
+      rows = next;
+      rows.read_ids(a, table, last_block);
+      copy_at(at[0], t0 + mine32, t1 + mine32);
+      if (n + key_waves < end) copy_at(at[1], t2 + mine32, t3 + mine32);
+    }
+    look_for_bad();
+    if (n < end) {
       const int whole = wk.any_bad ? 0 : min(end, all_see / 32);  // blocks that all rows see
       first_left_out = max(first_left_out, 32 * whole);
-      rows.start(a, 32 * n + f_row, R::kAtOnce, 32 * key_waves);
-      rows.read_ids(a, wk.table, last_block);
-      copy_block(t0 + mine32, t1 + mine32);
-      if (n + key_waves < end) copy_block(t2 + mine32, t3 + mine32);
       int odd_turn = 0;
       while (n < whole) {
         turn(t0 + mine32, t1 + mine32, std::false_type{}, lane);
@@ -520,98 +570,175 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
       }
     }
   } else {
-    // All waves go over all positions, 64 at a time.
-    const int lane = own_lane();
-    constexpr int kCopies = D / 64;                        // 1 KB copies of a wave of a tile's keys, or values
-    typedef Rows<D, kCopies> R;
-    const int f_row = wave * kCopies * R::kAtOnce + lane / R::kLanes, f_place = lane % R::kLanes;
-    R rows;
-    rows.start(a, pc.from * kTileKeys + f_row, R::kAtOnce, kTileKeys);
-    // Copies of the next tile, after the block numbers of the one behind it: what waits for those
-    // need not wait for the copies.
-    auto copy_next = [&](uint8_t* to) {
-      int64_t at[kCopies];
+    // The waves share what is copied, four steps in LDS: of 64 positions, whose rows all waves go over,
+    // or, with two waves of rows, of two times 32 positions (of two KV heads, or in a row), which two
+    // waves each go over.
+    auto go = [&](auto blocks) {
+      constexpr int kBlocks = decltype(blocks)::value;
+      constexpr int kRows = kBlocks == 2 ? D / 64 : D / 32;   // rows that a lane copies, of keys and values or of either
+      constexpr int kCopies = D / 32;                         // copies of a wave and step
+      typedef Rows<D, kRows> R;
+      const int lane = own_lane();
+      const ChunkArgs& a = own_args();
+      const int sub = kBlocks == 2 ? 0 : wave >> 1, side = wave & 1;
+      const int step = kBlocks == 2 ? kTileKeys : 32 * key_waves;
+      const int keys_at = sub * 64 * D, values_at = keys_at + (kBlocks == 2 ? kTileBytes : 32 * D);
+      // the first position that this wave goes over
+      const int start = pc.from * kTileKeys + (kBlocks == 1 && key_waves == 2 ? 32 * sub : 0);
+      const int f_row = (kBlocks == 2 ? wave * kRows * R::kAtOnce : 0) + lane / R::kLanes, f_place = lane % R::kLanes;
+      R rows;
+      rows.start(a, start + f_row, R::kAtOnce, step);
+      // Copies of the next step, after the block numbers of the one behind it: what waits for those
+      // need not wait for the copies.
+      auto copy_step = [&](const int64_t* at, uint8_t* to) {
 #pragma unroll
-      for (int j = 0; j < kCopies; ++j) at[j] = rows.place(a, j);
-      rows.read_ids(a, wk.table, last_block);
-#pragma unroll
-      for (int j = 0; j < kCopies; ++j) {
-        const int r = f_row + j * R::kAtOnce;
-        copy16(kc + at[j] + (f_place ^ key_turn<D>(r)) * 16, to + (wave * kCopies + j) * 1024);
-        copy16(vc + at[j] + (f_place ^ value_turn<D>(r)) * 16, to + kTileBytes + (wave * kCopies + j) * 1024);
+        for (int j = 0; j < kRows; ++j) {
+          const int r = f_row + j * R::kAtOnce;
+          const int k = (f_place ^ key_turn<D>(r)) * 16, v = (f_place ^ value_turn<D>(r)) * 16;
+          if constexpr (kBlocks == 2) {
+            copy16(kc + at[j] + k, to + (wave * kRows + j) * 1024);
+            copy16(vc + at[j] + v, to + kTileBytes + (wave * kRows + j) * 1024);
+          } else {  // one of the two waves copies keys, the other values
+            copy16((side ? vc + v : kc + k) + at[j], to + (side ? values_at : keys_at) + j * 1024);
+          }
+        }
+      };
+      auto copy_next = [&](uint8_t* to) {
+        int64_t at[kRows];
+        rows.places(a, at);
+        rows.read_ids(a, table, last_block);
+        asm volatile("" ::: "memory");
+        copy_step(at, to);
+      };
+      const int steps = (min(pc.to * kTileKeys, pc.len) - pc.from * kTileKeys + step - 1) / step;
+      if (steps > 0) {
+        // (the first steps' block numbers are read all at once)
+        rows.read_ids(a, table, last_block);
+        R next = rows;
+        next.read_ids(a, table, last_block);
+        R third = next;
+        third.read_ids(a, table, last_block);
+        int64_t at[3][kRows];
+        rows.places(a, at[0]);
+        next.places(a, at[1]);
+        third.places(a, at[2]);
+        rows = third;
+        rows.read_ids(a, table, last_block);
+        copy_step(at[0], t0);
+        copy_step(at[1], t1);
+        copy_step(at[2], t2);
       }
-    };
-    const int tiles = pc.to - pc.from;
-    const int whole = wk.any_bad ? 0 : all_see / kTileKeys - pc.from;   // tiles that all rows see
-    float base = 0.0f;
-    // At the barrier of tile t all waves' copies of tile t + 1 have landed (at most those of t + 2
-    // have not), and the tile before t has been read by all: tile t + 3 takes its place.
-    auto next_tile = [&](uint8_t* free) {
-      asm volatile("" ::: "memory");
-      __builtin_amdgcn_s_waitcnt(until_vmcnt(2 * kCopies));
-      __syncthreads();
-      copy_next(free);
-    };
-    auto scores = [&](int t, v16f* s, const uint8_t* kt, int lane) {
-      code_scores<D, 2>(s, kt, qf, lane);
-      const int p0 = (pc.from + t) * kTileKeys;
-      if (p0 + kTileKeys > wave_least || wk.any_bad) wk.template mask<2>(s, p0, limit);
-      base = sums.template move_to<2>(largest_score<2>(s) * scale, s, scale);
-    };
-    // Tile t, whose scores are s, while the whole tiles last: the scores of t + 1 (matrix cores) beside
-    // the weights of t (vector ALUs), then the values of t beside the largest of the new scores.
-    auto turn = [&](const v16f* s, v16f* next, const uint8_t* here, const uint8_t* then, uint8_t* free) {
-      next_tile(free);
-      code_scores<D, 2>(next, then, qf, lane);
-      v8bf p[4];
+      look_for_bad();
+      if (steps <= 0) return;
+      // steps that all rows see
+      const int whole = wk.any_bad ? 0 : max(all_see - pc.from * kTileKeys, 0) / step;
+      float base = 0.0f;
+      // At the barrier of step t all waves' copies of step t + 1 have landed (at most those of t + 2
+      // have not), and the step before t has been read by all: step t + 3 takes its place.
+      // (nothing is written to LDS but by copies, and what was read has been used: no fence is needed,
+      // which would wait for all copies)
+      auto next_step = [&](auto wait) {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(decltype(wait)::value);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+      };
+      auto scores = [&](int t, v16f* s, const uint8_t* then, int lane) {
+        code_scores<D, kBlocks>(s, then + keys_at, qf, lane);
+        const int p0 = start + t * step;
+        if (p0 + 32 * kBlocks > wave_least || wk.any_bad) wk.template mask<kBlocks>(s, p0, limit);
+        base = sums.template move_to<kBlocks>(largest_score<kBlocks>(s) * scale, s, scale);
+      };
+      // Step t, whose scores are s, while the whole ones last: the scores of t + 1 (matrix cores) beside
+      // the weights of t (vector ALUs), then the values of t beside the largest of the new scores.
+      auto turn = [&](const v16f* s, v16f* next, const uint8_t* here, const uint8_t* then, uint8_t* free) {
+        next_step(std::integral_constant<int, until_vmcnt(kCopies)>{});
+        constexpr int kKeys = D / 32, kSteps = 2 * kBlocks;
+        uint4 x[2][kBlocks];
+        v2u y[2][D / 32];
+        v8bf p[kSteps];
+        auto read_keys = [&](int c) {
 #pragma unroll
-      for (int st = 0; st < 4; ++st) p[st] = sums.weights(s[st >> 1], st & 1, scale, base);
+          for (int b = 0; b < kBlocks; ++b) x[c & 1][b] = key_codes<D>(then + keys_at, c, b, lane);
+        };
+        auto read_values = [&](int st) {
 #pragma unroll
-      for (int st = 0; st < 4; ++st) sums.template add_values<false>(here + kTileBytes, st, p[st], &odd, lane);
-      const float top = largest_score<2>(next);
-      if constexpr (D == 128) pair_up<D>();
-      base = sums.template move_to<2>(top * scale, next, scale);
-    };
-    if (tiles > 0) {
-      v16f sa[2];
-      rows.read_ids(a, wk.table, last_block);
-      copy_next(t0);
-      copy_next(t1);
-      copy_next(t2);
-      asm volatile("" ::: "memory");
-      __builtin_amdgcn_s_waitcnt(until_vmcnt(4 * kCopies));
-      __syncthreads();
+          for (int i = 0; i < D / 32; ++i) y[st & 1][i] = value_codes<D>(here + values_at, st, i, lane);
+        };
+        read_keys(0);
+        copy_next(free);
+        p[0] = sums.weights(s[0], 0, scale, base);
+        clear<kBlocks>(next);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int c = 0; c < kKeys; ++c) {
+          if (c + 1 < kKeys) read_keys(c + 1); else read_values(0);
+          add_scores<kBlocks>(next, x[c & 1], qf, c);
+          if (c + 1 < kSteps) p[c + 1] = sums.weights(s[(c + 1) >> 1], (c + 1) & 1, scale, base);
+          if (c + 1 < kKeys) in_order<kBlocks, 2 * kBlocks + 2, 9>(); else in_order<D / 32, 2 * kBlocks, 4>();
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st) {
+          if (st + 1 < kSteps) read_values(st + 1);
+          if (st > kKeys) p[st] = sums.weights(s[st >> 1], st & 1, scale, base);
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i)
+            sums.o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_bf16(y[st & 1][i][0], y[st & 1][i][1]), p[st], sums.o[i], 0, 0, 0);
+          if (st + 1 < kSteps) {
+            in_order<D / 32, D / 32, 6>();
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+        const float top = largest_score<kBlocks>(next);
+        base = sums.template move_to<kBlocks>(top * scale, next, scale);
+      };
+      v16f sa[kBlocks];
+      next_step(std::integral_constant<int, until_vmcnt(2 * kCopies)>{});
       scores(0, sa, t0, lane);
       int t = 0;
-      while (t + 2 < whole && t + 2 < tiles) {
-        v16f sb[2];
+      const int most = min(whole, steps) - 1;  // steps whose next one is whole
+      while (t < most) {
+        v16f sb[kBlocks];
+        auto out = [&]() {
+          if (++t < most) return false;
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b) sa[b] = sb[b];
+          return true;
+        };
         turn(sa, sb, t0, t1, t3);
+        if (out()) break;
         turn(sb, sa, t1, t2, t0);
-        t += 2;
-        if (!(t + 2 < whole && t + 2 < tiles)) break;
+        if (++t >= most) break;
         turn(sa, sb, t2, t3, t1);
+        if (out()) break;
         turn(sb, sa, t3, t0, t2);
-        t += 2;
+        ++t;
       }
-      first_left_out += t * kTileKeys;
-      for (; t < tiles; ++t) {  // the last tiles, among them those that are seen in part
+      first_left_out += t * step;
+      for (; t < steps; ++t) {  // the last steps, among them those that are seen in part
         const int lane = own_lane();
         auto slot_of = [&](int i) { return i & 2 ? i & 1 ? t3 : t2 : i & 1 ? t1 : t0; };
-        next_tile(slot_of(t + 3));
+        next_step(std::integral_constant<int, until_vmcnt(0)>{});
+        if (t + 3 < steps) copy_next(slot_of(t + 3));
 #pragma unroll
-        for (int st = 0; st < 4; ++st)
-          sums.template add_values<true>(slot_of(t) + kTileBytes, st, sums.weights(sa[st >> 1], st & 1, scale, base), &odd, lane);
+        for (int st = 0; st < 2 * kBlocks; ++st)
+          sums.template add_values<true>(slot_of(t) + values_at, st, sums.weights(sa[st >> 1], st & 1, scale, base), &odd, lane);
         __builtin_amdgcn_sched_barrier(0);
-        if (t + 1 < tiles) scores(t + 1, sa, slot_of(t + 1), lane);
+        if (t + 1 < steps) scores(t + 1, sa, slot_of(t + 1), lane);
       }
-      __builtin_amdgcn_s_waitcnt(until_vmcnt(0));  // copies behind the last tile: LDS is used again
-    }
+    };
+    if (row_waves == 4) go(std::integral_constant<int, 2>{});
+    else go(std::integral_constant<int, 1>{});
   }
 
   // NaN codes that were left out reach the rows that see them.
+  tell(1, odd != 0);
   __syncthreads();
-  if (any_of_all(odd != 0) && key_wave == 0) wk.take_nans(sums, first_left_out, limit);
+  if (told(1) && key_wave == 0) wk.take_nans(sums, first_left_out, limit);
 
+  {
+  const ChunkArgs& a = own_args();
   float ref = sums.ref, total = sum_over_halves(sums.sum), of_rounded = sum_over_halves(sums.rounded[0]);
   v16f* const o = sums.o;
   // Waves that took different positions of the same rows add up in pairs, through LDS.
@@ -673,6 +800,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
       *reinterpret_cast<uint2*>(a.out + q_row * a.os + int64_t(my_head) * D + 32 * i + 2 * r + 4 * half) =
           make_uint2(cvt_bf16x2(o[i][r] * inv, o[i][r + 1] * inv),
                      cvt_bf16x2(o[i][r + 2] * inv, o[i][r + 3] * inv));
+  }
 }
 
 // Adds up the parts of a piece in order.  The workgroups of each part take a share of its rows, D/4 lanes
@@ -680,16 +808,19 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
 // workgroup's row.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinGroups = 8;   // workgroups of a part
+constexpr int kJoinPerCu = 8;    // workgroups on a compute unit
 constexpr int kManyParts = 16;
 template <int D>
 __global__ __launch_bounds__(kJoinThreads) void chunk_join_kernel(const ChunkArgs a) {
   constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
-  const int slot = blockIdx.x / kJoinGroups;
-  if (slot >= a.parts[a.slots * a.hkv].x) return;
+  const int used = a.parts[a.slots * a.hkv].x;
+  for (int item = blockIdx.x; item < a.slots * a.hkv * kJoinGroups; item += gridDim.x) {
+  const int slot = item / kJoinGroups;
   const int4 x = a.parts[slot];
+  if (slot >= used) return;
   const int part = x.w & 0xFFFF, parts = x.w >> 16;
   const int rows = x.z & 0xFF, row_waves = x.z >> 8 & 0xF, heads = x.z >> 12 & 0xF, kvh = int(uint32_t(x.z) >> 16);
-  const int share = part * kJoinGroups + blockIdx.x % kJoinGroups, shares = parts * kJoinGroups;
+  const int share = part * kJoinGroups + item % kJoinGroups, shares = parts * kJoinGroups;
   const int group = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
   const int64_t first = int64_t(slot - part) * kTileRows;  // a piece's parts lie side by side
   const bool many = parts > kManyParts;
@@ -744,6 +875,7 @@ __global__ __launch_bounds__(kJoinThreads) void chunk_join_kernel(const ChunkArg
         make_uint2(cvt_bf16x2(v.x * inv, v.y * inv), cvt_bf16x2(v.z * inv, v.w * inv));
     if (a.lse && d == 0)
       a.lse[q_row * a.hq + head] = total == 0.0f ? neg_inf() : (ref + __builtin_amdgcn_logf(total)) * kLn2;
+  }
   }
 }
 
@@ -857,6 +989,7 @@ extern "C" int fp8_attn_chunk(const uint16_t* q, const uint8_t* k_cache, const u
   if (launch_status() != FP8Q_OK || p.slots == 0) return launch_status();
   auto join = head_dim == 64 ? chunk_join_kernel<64>
               : head_dim == 128 ? chunk_join_kernel<128> : chunk_join_kernel<256>;
-  launch(join, dim3(unsigned(p.slots * num_kv_heads * kJoinGroups)), dim3(kJoinThreads), 0, stream, a);
+  const int joins = p.slots * num_kv_heads * kJoinGroups, most = kJoinPerCu * num_cus();
+  launch(join, dim3(unsigned(joins < most ? joins : most)), dim3(kJoinThreads), 0, stream, a);
   return launch_status();
 }

@@ -35,27 +35,43 @@ __device__ __forceinline__ v8bf e4m3x8_to_bf16(uint32_t lo, uint32_t hi) {
                                       e4m3x2_to_bf16<false>(hi), e4m3x2_to_bf16<true>(hi)});
 }
 
-// S^T of 32 kBlocks keys whose codes lie in LDS; a pair of steps takes 32 values of a row, 16 for each
-// half, so the queries' fragments 2 c and 2 c + 1 hold values 32 c + 16 half .. + 7 and + 8 .. + 15.
-template <int D, int kBlocks>
-__device__ __forceinline__ void code_scores(v16f* s, const uint8_t* ks, const v8bf* qf, int lane) {
+// Codes of 32 keys (block b of those in LDS), values 32 c + 16 half .. + 15.
+template <int D>
+__device__ __forceinline__ uint4 key_codes(const uint8_t* ks, int c, int b, int lane) {
   const int col = lane & 31, half = lane >> 5;
+  return *reinterpret_cast<const uint4*>(ks + (32 * b + col) * D + ((2 * c + half) ^ key_turn<D>(col)) * 16);
+}
+
+// Adds their products to the scores S^T; the queries' fragments 2 c and 2 c + 1 hold values 32 c + 16 half
+// .. + 7 and + 8 .. + 15.
+template <int kBlocks>
+__device__ __forceinline__ void add_scores(v16f* s, const uint4* x, const v8bf* qf, int c) {
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b)
+    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_bf16(x[b].x, x[b].y), qf[2 * c], s[b], 0, 0, 0);
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b)
+    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_bf16(x[b].z, x[b].w), qf[2 * c + 1], s[b], 0, 0, 0);
+}
+
+template <int kBlocks>
+__device__ __forceinline__ void clear(v16f* s) {
 #pragma unroll
   for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
     for (int r = 0; r < 16; ++r) s[b][r] = 0.0f;
+}
+
+// S^T of 32 kBlocks keys whose codes lie in LDS.
+template <int D, int kBlocks>
+__device__ __forceinline__ void code_scores(v16f* s, const uint8_t* ks, const v8bf* qf, int lane) {
+  clear<kBlocks>(s);
 #pragma unroll
   for (int c = 0; c < D / 32; ++c) {
     uint4 x[kBlocks];
 #pragma unroll
-    for (int b = 0; b < kBlocks; ++b)
-      x[b] = *reinterpret_cast<const uint4*>(ks + (32 * b + col) * D + ((2 * c + half) ^ key_turn<D>(col)) * 16);
-#pragma unroll
-    for (int b = 0; b < kBlocks; ++b)
-      s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_bf16(x[b].x, x[b].y), qf[2 * c], s[b], 0, 0, 0);
-#pragma unroll
-    for (int b = 0; b < kBlocks; ++b)
-      s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_bf16(x[b].z, x[b].w), qf[2 * c + 1], s[b], 0, 0, 0);
+    for (int b = 0; b < kBlocks; ++b) x[b] = key_codes<D>(ks, c, b, lane);
+    add_scores<kBlocks>(s, x, qf, c);
   }
 }
 
