@@ -26,7 +26,7 @@ constexpr int kFewRows = 64;     // so many rows of a sequence and KV head at mo
 constexpr int kMinPart = 4;      // tiles of positions of a part, at least
 constexpr int kMinFewPart = 1;   // the same of few rows
 // Times, in that of a tile of positions of a workgroup of many rows that shares its compute unit:
-constexpr float kFewCost = 0.6f;    // a tile of positions of few rows, for each KV head
+constexpr float kFewCost = 0.8f;    // a tile of positions of few rows, for each KV head
 constexpr float kAloneCost = 0.6f;  // a tile of a workgroup alone on its compute unit
 constexpr float kPieceCost = 2.0f;  // a workgroup's start and end
 constexpr float kJoinCost = 0.011f; // a part's sums, written and read again
@@ -380,18 +380,6 @@ __device__ __forceinline__ void copy16(const uint8_t* from, uint8_t* to) {
 // s_waitcnt's operand for vmcnt(n).
 constexpr int until_vmcnt(int n) { return (n & 15) | (n >> 4) << 14 | 0x0F70; }
 
-// The order of a step of a turn: the LDS reads of the next one, then products with vector instructions
-// between them.
-template <int kReads, int kProducts, int kVectors>
-__device__ __forceinline__ void in_order() {
-  __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
-  if constexpr (kProducts > 0) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x002, kVectors, 0);
-    in_order<0, kProducts - 1, kVectors>();
-  }
-}
-
 template <int D>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chunk_kernel(const ChunkArgs) {
   const ChunkArgs& a = own_args();
@@ -449,8 +437,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
   const int my_row = min(row, pc.rows - 1), my_query = query_of(my_row);
   const int my_head = kvh * a.group + pc.row0 + my_row - my_query * a.group;
   const int limit = row < pc.rows ? pc.seen(a, my_query) : 0;
-  // positions that all rows of the wave see, and that all rows of the tile see
-  const int wave_least = __builtin_amdgcn_readfirstlane(mine + kWaveRows <= pc.rows ? pc.seen(a, query_of(mine)) : 0);
+  // positions that all rows of the tile see
   const int all_see = __builtin_amdgcn_readfirstlane(pc.seen(a, query_of(0)));
 
   v8bf qf[D / 16];
@@ -483,6 +470,31 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
   const uint8_t* const kc = a.kc + int64_t(kvh) * D;
   const uint8_t* const vc = a.vc + int64_t(kvh) * D;
 
+  // A wave's rows over 32 kBlocks positions from p0 on, whose codes lie in LDS; with kEdge they may be
+  // seen in part.
+  auto attend = [&](const uint8_t* ks, const uint8_t* vs, int p0, auto blocks, auto edge, int lane) __attribute__((always_inline)) {
+    constexpr int kBlocks = decltype(blocks)::value;
+    constexpr bool kEdge = decltype(edge)::value;
+    v16f s[kBlocks];
+    code_scores<D, kBlocks>(s, ks, qf, lane);
+    // values are read before the weights are made, as registers allow
+    constexpr int kSteps = 2 * kBlocks, kEarly = D == 256 ? 0 : kSteps;
+    v2u y[kSteps][D / 32];
+    auto read_values = [&](int st) {
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) y[st][i] = value_codes<D>(vs, st, i, lane);
+    };
+#pragma unroll
+    for (int st = 0; st < kEarly; ++st) read_values(st);
+    if constexpr (kEdge) wk.template mask<kBlocks>(s, p0, limit);
+    const float base = sums.template move_to<kBlocks>(largest_score<kBlocks>(s) * scale, s, scale);
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st) {
+      if (st >= kEarly) read_values(st);
+      sums.template add_values<kEdge>(y[st], sums.weights(s[st >> 1], st & 1, scale, base), &odd);
+    }
+  };
+
   if (row_waves == 1) {
     // Each wave takes every key_waves-th block of 32 positions, two blocks ahead in LDS.
     const int lane = own_lane();
@@ -510,25 +522,14 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
       asm volatile("" ::: "memory");
       copy_at(at, ks, vs);
     };
-    // Block n; with kEdge it may be seen in part.
-    auto block = [&](const uint8_t* ks, const uint8_t* vs, auto edge, int lane) {
-      constexpr bool kEdge = decltype(edge)::value;
-      v16f s[1];
-      code_scores<D, 1>(s, ks, qf, lane);
-      if (kEdge) wk.template mask<1>(s, 32 * n, limit);
-      const float base = sums.template move_to<1>(largest_score<1>(s) * scale, s, scale);
-#pragma unroll
-      for (int st = 0; st < 2; ++st)
-        sums.template add_values<kEdge>(vs, st, sums.weights(s[0], st, scale, base), &odd, lane);
-    };
     // Waits for block n, takes it, and copies the one after the next into its place.
-    auto turn = [&](uint8_t* ks, uint8_t* vs, auto edge, int lane) {
+    auto turn = [&](uint8_t* ks, uint8_t* vs, auto edge, int lane) __attribute__((always_inline)) {
       asm volatile("" ::: "memory");
       // this block's copies have landed: at most the next one's have not
       if (n + key_waves < end) __builtin_amdgcn_s_waitcnt(until_vmcnt(2 * kCopies));
       else __builtin_amdgcn_s_waitcnt(until_vmcnt(0));
       asm volatile("" ::: "memory");
-      block(ks, vs, edge, lane);
+      attend(ks, vs, 32 * n, std::integral_constant<int, 1>{}, edge, lane);
       if (n + 2 * key_waves < end) {
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this block has been read
         asm volatile("" ::: "memory");
@@ -573,7 +574,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
     // The waves share what is copied, four steps in LDS: of 64 positions, whose rows all waves go over,
     // or, with two waves of rows, of two times 32 positions (of two KV heads, or in a row), which two
     // waves each go over.
-    auto go = [&](auto blocks) {
+    auto go = [&](auto blocks) __attribute__((always_inline)) {
       constexpr int kBlocks = decltype(blocks)::value;
       constexpr int kRows = kBlocks == 2 ? D / 64 : D / 32;   // rows that a lane copies, of keys and values or of either
       constexpr int kCopies = D / 32;                         // copies of a wave and step
@@ -632,101 +633,37 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
       if (steps <= 0) return;
       // steps that all rows see
       const int whole = wk.any_bad ? 0 : max(all_see - pc.from * kTileKeys, 0) / step;
-      float base = 0.0f;
-      // At the barrier of step t all waves' copies of step t + 1 have landed (at most those of t + 2
-      // have not), and the step before t has been read by all: step t + 3 takes its place.
-      // (nothing is written to LDS but by copies, and what was read has been used: no fence is needed,
-      // which would wait for all copies)
-      auto next_step = [&](auto wait) {
+      // Step t: at its barrier all waves' copies of it have landed (at most those of the two after it have
+      // not), and the step before it has been read by all: step t + 3 takes its place.  (Nothing is
+      // written to LDS but by copies, and what was read has been used: no fence is needed, which would
+      // wait for all copies.)  With kEdge it may be seen in part.
+      int t = 0;
+      auto turn = [&](const uint8_t* here, uint8_t* free, auto edge, int lane) __attribute__((always_inline)) {
+        constexpr bool kEdge = decltype(edge)::value;
         asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(decltype(wait)::value);
+        __builtin_amdgcn_s_waitcnt(until_vmcnt(kEdge ? 0 : 2 * kCopies));
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-      };
-      auto scores = [&](int t, v16f* s, const uint8_t* then, int lane) {
-        code_scores<D, kBlocks>(s, then + keys_at, qf, lane);
-        const int p0 = start + t * step;
-        if (p0 + 32 * kBlocks > wave_least || wk.any_bad) wk.template mask<kBlocks>(s, p0, limit);
-        base = sums.template move_to<kBlocks>(largest_score<kBlocks>(s) * scale, s, scale);
-      };
-      // Step t, whose scores are s, while the whole ones last: the scores of t + 1 (matrix cores) beside
-      // the weights of t (vector ALUs), then the values of t beside the largest of the new scores.
-      auto turn = [&](const v16f* s, v16f* next, const uint8_t* here, const uint8_t* then, uint8_t* free) {
-        next_step(std::integral_constant<int, until_vmcnt(kCopies)>{});
-        constexpr int kKeys = D / 32, kSteps = 2 * kBlocks;
-        uint4 x[2][kBlocks];
-        v2u y[2][D / 32];
-        v8bf p[kSteps];
-        auto read_keys = [&](int c) {
-#pragma unroll
-          for (int b = 0; b < kBlocks; ++b) x[c & 1][b] = key_codes<D>(then + keys_at, c, b, lane);
-        };
-        auto read_values = [&](int st) {
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) y[st & 1][i] = value_codes<D>(here + values_at, st, i, lane);
-        };
-        read_keys(0);
-        copy_next(free);
-        p[0] = sums.weights(s[0], 0, scale, base);
-        clear<kBlocks>(next);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int c = 0; c < kKeys; ++c) {
-          if (c + 1 < kKeys) read_keys(c + 1); else read_values(0);
-          add_scores<kBlocks>(next, x[c & 1], qf, c);
-          if (c + 1 < kSteps) p[c + 1] = sums.weights(s[(c + 1) >> 1], (c + 1) & 1, scale, base);
-          if (c + 1 < kKeys) in_order<kBlocks, 2 * kBlocks + 2, 9>(); else in_order<D / 32, 2 * kBlocks, 4>();
-          __builtin_amdgcn_sched_barrier(0);
-        }
-#pragma unroll
-        for (int st = 0; st < kSteps; ++st) {
-          if (st + 1 < kSteps) read_values(st + 1);
-          if (st > kKeys) p[st] = sums.weights(s[st >> 1], st & 1, scale, base);
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i)
-            sums.o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_bf16(y[st & 1][i][0], y[st & 1][i][1]), p[st], sums.o[i], 0, 0, 0);
-          if (st + 1 < kSteps) {
-            in_order<D / 32, D / 32, 6>();
-            __builtin_amdgcn_sched_barrier(0);
-          }
-        }
-        const float top = largest_score<kBlocks>(next);
-        base = sums.template move_to<kBlocks>(top * scale, next, scale);
-      };
-      v16f sa[kBlocks];
-      next_step(std::integral_constant<int, until_vmcnt(2 * kCopies)>{});
-      scores(0, sa, t0, lane);
-      int t = 0;
-      const int most = min(whole, steps) - 1;  // steps whose next one is whole
-      while (t < most) {
-        v16f sb[kBlocks];
-        auto out = [&]() {
-          if (++t < most) return false;
-#pragma unroll
-          for (int b = 0; b < kBlocks; ++b) sa[b] = sb[b];
-          return true;
-        };
-        turn(sa, sb, t0, t1, t3);
-        if (out()) break;
-        turn(sb, sa, t1, t2, t0);
-        if (++t >= most) break;
-        turn(sa, sb, t2, t3, t1);
-        if (out()) break;
-        turn(sb, sa, t3, t0, t2);
+        if (!kEdge || t + 3 < steps) copy_next(free);
+        attend(here + keys_at, here + values_at, start + t * step, blocks, edge, lane);
         ++t;
+      };
+      const int most = min(whole, steps);
+      while (t < most) {
+        turn(t0, t3, std::false_type{}, lane);
+        if (t >= most) break;
+        turn(t1, t0, std::false_type{}, lane);
+        if (t >= most) break;
+        turn(t2, t1, std::false_type{}, lane);
+        if (t >= most) break;
+        turn(t3, t2, std::false_type{}, lane);
       }
       first_left_out += t * step;
-      for (; t < steps; ++t) {  // the last steps, among them those that are seen in part
-        const int lane = own_lane();
+      while (t < steps) {  // the last steps, which may be seen in part
         auto slot_of = [&](int i) { return i & 2 ? i & 1 ? t3 : t2 : i & 1 ? t1 : t0; };
-        next_step(std::integral_constant<int, until_vmcnt(0)>{});
-        if (t + 3 < steps) copy_next(slot_of(t + 3));
-#pragma unroll
-        for (int st = 0; st < 2 * kBlocks; ++st)
-          sums.template add_values<true>(slot_of(t) + values_at, st, sums.weights(sa[st >> 1], st & 1, scale, base), &odd, lane);
-        __builtin_amdgcn_sched_barrier(0);
-        if (t + 1 < steps) scores(t + 1, sa, slot_of(t + 1), lane);
+        turn(slot_of(t), slot_of(t + 3), std::true_type{}, own_lane());
       }
+      __builtin_amdgcn_s_waitcnt(until_vmcnt(0));  // copies behind the last step: LDS is used again
     };
     if (row_waves == 4) go(std::integral_constant<int, 2>{});
     else go(std::integral_constant<int, 1>{});

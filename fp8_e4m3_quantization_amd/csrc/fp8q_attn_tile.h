@@ -42,36 +42,27 @@ __device__ __forceinline__ uint4 key_codes(const uint8_t* ks, int c, int b, int 
   return *reinterpret_cast<const uint4*>(ks + (32 * b + col) * D + ((2 * c + half) ^ key_turn<D>(col)) * 16);
 }
 
-// Adds their products to the scores S^T; the queries' fragments 2 c and 2 c + 1 hold values 32 c + 16 half
-// .. + 7 and + 8 .. + 15.
-template <int kBlocks>
-__device__ __forceinline__ void add_scores(v16f* s, const uint4* x, const v8bf* qf, int c) {
+// S^T of 32 kBlocks keys whose codes lie in LDS; the queries' fragments 2 c and 2 c + 1 hold values
+// 32 c + 16 half .. + 7 and + 8 .. + 15.
+template <int D, int kBlocks>
+__device__ __forceinline__ void code_scores(v16f* s, const uint8_t* ks, const v8bf* qf, int lane) {
+  uint4 x[D / 32][kBlocks];
 #pragma unroll
-  for (int b = 0; b < kBlocks; ++b)
-    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_bf16(x[b].x, x[b].y), qf[2 * c], s[b], 0, 0, 0);
+  for (int c = 0; c < D / 32; ++c)
 #pragma unroll
-  for (int b = 0; b < kBlocks; ++b)
-    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_bf16(x[b].z, x[b].w), qf[2 * c + 1], s[b], 0, 0, 0);
-}
-
-template <int kBlocks>
-__device__ __forceinline__ void clear(v16f* s) {
+    for (int b = 0; b < kBlocks; ++b) x[c][b] = key_codes<D>(ks, c, b, lane);
 #pragma unroll
   for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
     for (int r = 0; r < 16; ++r) s[b][r] = 0.0f;
-}
-
-// S^T of 32 kBlocks keys whose codes lie in LDS.
-template <int D, int kBlocks>
-__device__ __forceinline__ void code_scores(v16f* s, const uint8_t* ks, const v8bf* qf, int lane) {
-  clear<kBlocks>(s);
 #pragma unroll
   for (int c = 0; c < D / 32; ++c) {
-    uint4 x[kBlocks];
 #pragma unroll
-    for (int b = 0; b < kBlocks; ++b) x[b] = key_codes<D>(ks, c, b, lane);
-    add_scores<kBlocks>(s, x, qf, c);
+    for (int b = 0; b < kBlocks; ++b)
+      s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_bf16(x[c][b].x, x[c][b].y), qf[2 * c], s[b], 0, 0, 0);
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b)
+      s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_bf16(x[c][b].z, x[c][b].w), qf[2 * c + 1], s[b], 0, 0, 0);
   }
 }
 
@@ -172,12 +163,13 @@ struct RowSums {
     rounded = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(ones, __builtin_bit_cast(v4s, v2u{w[2], w[3]}), rounded, 0, 0, 0);
     return __builtin_bit_cast(v8bf, v4u{w[0], w[1], w[2], w[3]});
   }
-  // o^T += V^T P^T over 16 keys.  With kClean NaN codes are left out (and `odd` tells).
+  // o^T += V^T P^T over 16 keys, whose values' codes are y.  With kClean NaN codes are left out (and
+  // `odd` tells).
   template <bool kClean>
-  __device__ __forceinline__ void add_values(const uint8_t* vs, int st, v8bf p, uint32_t* odd, int lane) {
+  __device__ __forceinline__ void add_values(const v2u* y, v8bf p, uint32_t* odd) {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-      v2u w = value_codes<D>(vs, st, i, lane);
+      v2u w = y[i];
       if (kClean) w = v2u{without_nans(w[0], odd), without_nans(w[1], odd)};
       o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_bf16(w[0], w[1]), p, o[i], 0, 0, 0);
     }
