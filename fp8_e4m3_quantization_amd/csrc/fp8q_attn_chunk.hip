@@ -487,11 +487,12 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
 #pragma unroll
     for (int st = 0; st < kEarly; ++st) read_values(st);
     if constexpr (kEdge) wk.template mask<kBlocks>(s, p0, limit);
-    const float base = sums.template move_to<kBlocks>(largest_score<kBlocks>(s) * scale, s, scale);
+    v8bf p[kSteps];
+    sums.template weigh<kBlocks, kEdge>(s, scale, p);
 #pragma unroll
     for (int st = 0; st < kSteps; ++st) {
       if (st >= kEarly) read_values(st);
-      sums.template add_values<kEdge>(y[st], sums.weights(s[st >> 1], st & 1, scale, base), &odd);
+      sums.template add_values<kEdge>(y[st], p[st], &odd);
     }
   };
 

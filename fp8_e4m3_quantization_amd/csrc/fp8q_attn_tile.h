@@ -15,6 +15,7 @@ __device__ __forceinline__ int own_lane() {
 
 constexpr int kTileKeys = 64;
 constexpr int kWaveRows = 32;
+constexpr float kMostWeights = 0x1p13f;  // 32 weights of 2^kSoftmaxSlack, a lane's of 64 keys
 constexpr float kFar = 0x1p27f;  // a reference whose rounding (2^3) still leaves weights their range
 
 typedef short v4s __attribute__((ext_vector_type(4)));
@@ -108,6 +109,7 @@ struct RowSums {
   v16f o[D / 32];
   float ref, sum;
   v4f rounded;
+  bool far;  // some row's reference is
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
@@ -116,6 +118,7 @@ struct RowSums {
     ref = neg_inf();
     sum = 0.0f;
     rounded = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    far = false;
   }
   // The reference for scores s, whose largest is top (log2 units).  Returns what weights subtract.
   // Where s * scale - ref is one fused product it is exact but for its last rounding, while ref is
@@ -136,7 +139,8 @@ struct RowSums {
         for (int r = 0; r < 16; ++r) o[i][r] *= f;
     }
     const float base = ref == neg_inf() ? 0.0f : ref;
-    if (kFused && __any(__builtin_fabsf(base) > kFar)) {
+    far = kFused && __any(__builtin_fabsf(base) > kFar);
+    if (far) {
       const float back = 1.0f / scale;
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b)
@@ -149,29 +153,59 @@ struct RowSums {
   static __device__ __forceinline__ float weight(float s, float scale, float base) {
     return __builtin_amdgcn_exp2f(kFused ? __builtin_fmaf(s, scale, -base) : s * scale - base);
   }
-  // Weights of 16 keys (half `h` of a block of scores) as the second product's operand.
-  __device__ __forceinline__ v8bf weights(const v16f& s, int h, float scale, float base) {
-    uint32_t w[4];
+  // Weights of the scores as the second product's operands, 16 keys each; returns their sum.
+  template <int kBlocks>
+  static __device__ __forceinline__ float weights_of(const v16f* s, float scale, float base, v8bf* p) {
+    float t = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-      const float x = weight(s[8 * h + e], scale, base), y = weight(s[8 * h + e + 1], scale, base);
-      sum += x + y;
-      w[e / 2] = cvt_bf16x2(x, y);
+    for (int st = 0; st < 2 * kBlocks; ++st) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const float x = weight(s[st >> 1][8 * (st & 1) + e], scale, base);
+        const float y = weight(s[st >> 1][8 * (st & 1) + e + 1], scale, base);
+        t += x + y;
+        w[e / 2] = cvt_bf16x2(x, y);
+      }
+      p[st] = __builtin_bit_cast(v8bf, v4u{w[0], w[1], w[2], w[3]});
     }
-    const v4s ones = {0x3F80, 0x3F80, 0x3F80, 0x3F80};
-    rounded = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(ones, __builtin_bit_cast(v4s, v2u{w[0], w[1]}), rounded, 0, 0, 0);
-    rounded = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(ones, __builtin_bit_cast(v4s, v2u{w[2], w[3]}), rounded, 0, 0, 0);
-    return __builtin_bit_cast(v8bf, v4u{w[0], w[1], w[2], w[3]});
+    return t;
+  }
+  // The weights of 32 kBlocks keys, all seen (kEdge: in part, scores of the others -infinity).  The largest
+  // score is looked for only where the weights against the present reference come too large (or
+  // there is none yet: infinite weights), or where references are far from 0: scores below the
+  // reference need no new one.
+  template <int kBlocks, bool kEdge>
+  __device__ __forceinline__ void weigh(v16f* s, float scale, v8bf* p) {
+    float t = 0.0f;
+    bool again = true;
+    if constexpr (!kEdge && kFused) {  // (256-wide heads have no registers for both ways)
+      if (far) {
+        again = true;
+      } else {
+        t = weights_of<kBlocks>(s, scale, ref, p);
+        again = __any(t > kMostWeights);
+      }
+    }
+    if (again) {
+      const float base = move_to<kBlocks>(largest_score<kBlocks>(s) * scale, s, scale);
+      t = weights_of<kBlocks>(s, scale, base, p);
+    }
+    sum += t;
   }
   // o^T += V^T P^T over 16 keys, whose values' codes are y.  With kClean NaN codes are left out (and
   // `odd` tells).
   template <bool kClean>
   __device__ __forceinline__ void add_values(const v2u* y, v8bf p, uint32_t* odd) {
+    const v4s ones = {0x3F80, 0x3F80, 0x3F80, 0x3F80};
+    const v4u w = __builtin_bit_cast(v4u, p);
+    rounded = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(ones, __builtin_bit_cast(v4s, v2u{w[0], w[1]}), rounded, 0, 0, 0);
+    rounded = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(ones, __builtin_bit_cast(v4s, v2u{w[2], w[3]}), rounded, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-      v2u w = y[i];
-      if (kClean) w = v2u{without_nans(w[0], odd), without_nans(w[1], odd)};
-      o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_bf16(w[0], w[1]), p, o[i], 0, 0, 0);
+      v2u c = y[i];
+      if (kClean) c = v2u{without_nans(c[0], odd), without_nans(c[1], odd)};
+      o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_bf16(c[0], c[1]), p, o[i], 0, 0, 0);
     }
   }
 };
