@@ -488,7 +488,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
     for (int st = 0; st < kEarly; ++st) read_values(st);
     if constexpr (kEdge) wk.template mask<kBlocks>(s, p0, limit);
     v8bf p[kSteps];
-    sums.template weigh<kBlocks, kEdge>(s, scale, p);
+    sums.template weigh<kBlocks>(s, scale, p);
 #pragma unroll
     for (int st = 0; st < kSteps; ++st) {
       if (st >= kEarly) read_values(st);
