@@ -207,9 +207,11 @@ __device__ __forceinline__ bool find_piece(const ChunkArgs& a, int kvh, int u, u
   bool found = false;
   int before = 0;
   *used = 0;
-  for (int order = 0; order < 2; ++order) {
+  // (without a limit no piece's time is long, and no part takes a slot)
+  const bool whole = most >= 1e9f;
+  for (int order = whole ? 1 : 0; order < 2; ++order) {
     int dealt2 = 0, dealt4 = 0, slots = 0;  // of the sequences so far
-    for (int s0 = 0; s0 < a.seqs; s0 += 64) {
+    for (int s0 = 0; s0 < a.seqs && !(whole && found); s0 += 64) {
       const Seq q = s0 == 0 ? first : Seq(a, s0 + lane);
       const int n = q.tiles(a), heads = q.heads(a), shift = heads >> 1;
       const float cost = float(q.steps()) * q.tile_cost(a);
