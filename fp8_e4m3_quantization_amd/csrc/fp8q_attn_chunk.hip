@@ -843,6 +843,7 @@ ChunkPlan chunk_plan(int32_t seqs, int32_t tq, int32_t hq, int32_t hkv, int32_t 
   // (with whole tiles for all slots nothing is split)
   if (seqs <= kSplitSeqs && slots > 3 && rows / kTileRows < slots) p.slots = slots;
   if (p.slots > p.pieces) p.pieces = p.slots;
+  if (p.slots == 0) return p;
   const uint64_t all = uint64_t(p.slots) * hkv * kTileRows;
   p.sums_bytes = all * d * 4;
   p.stats_bytes = all * 16;

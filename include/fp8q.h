@@ -541,8 +541,8 @@ int fp8_attn_decode(const uint16_t* q, const uint8_t* k_cache, const uint8_t* v_
  *               share one must not overlap in time; NULL is fine where the size is 0
  *   head_dim in {64, 128, 256}; num_q_heads a multiple of num_kv_heads; total_q * num_q_heads <=
  *   2^30; block_size > 0; num_seqs <= 65536; max_blocks * block_size <= 2^30; cache_stride >=
- *   block_size*H*D, a multiple of 16; q / out strides multiples of 8; k_scale, v_scale in
- *   [2^-64, 2^64]; 0 < softmax_scale <= 2^32.
+ *   block_size*H*D, a multiple of 16, below 2^32; q / out strides multiples of 8, up to 2^30;
+ *   k_scale, v_scale in [2^-64, 2^64]; 0 < softmax_scale <= 2^32.
  * The scores must stay within binary32.  Outputs must not overlap inputs.
  * Where the batch is too small to fill the GPU by its queries alone, histories are cut into parts:
  * then a workspace is needed and two kernels are enqueued, the second joining the parts in order
