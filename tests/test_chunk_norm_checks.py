@@ -29,7 +29,8 @@ def test_chunk_refusals():
                  dict(ts=7), dict(hq=0), dict(hq=7), dict(hkv=0), dict(d=80), dict(bs=0), dict(nb=0),
                  dict(mb=1 << 20, ts=1 << 20, bs=2048, cs=2048 * 256), dict(ks=0.0), dict(vs=-1.0),
                  dict(ks=NAN), dict(scale=0.0), dict(scale=NAN), dict(scale=INF), dict(qs=1000),
-                 dict(os=8), dict(cs=16 * 255), dict(cs=1 << 32), dict(os=(1 << 30) + 8), dict(ts=(1 << 40) + 1), dict(nb=1 << 62), dict(wb=16), dict(qs=(1 << 30) + 8)]:
+                 dict(os=8), dict(cs=16 * 255), dict(cs=1 << 32), dict(nb=1 << 62), dict(wb=16),
+                 dict(qs=(1 << 30) + 8), dict(os=(1 << 30) + 8), dict(ts=(1 << 40) + 1)]:
         assert _chunk(**over) == EINVAL, over
     for name in ("q", "kc", "vc", "tab", "lens", "cu", "out", "ws"):
         assert _chunk(**{name: None}) == ENULL, name
