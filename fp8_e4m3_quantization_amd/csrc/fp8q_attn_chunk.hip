@@ -379,8 +379,9 @@ __device__ __forceinline__ void copy16(const uint8_t* from, uint8_t* to) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from, (lds_void*)to, 16, 0, 0);
 }
 
-// s_waitcnt's operand for vmcnt(n).
+// s_waitcnt's operands for vmcnt(n), alone and with lgkmcnt(0).
 constexpr int until_vmcnt(int n) { return (n & 15) | (n >> 4) << 14 | 0x0F70; }
+constexpr int until_read_and_vmcnt(int n) { return until_vmcnt(n) & ~0x0F00; }
 
 template <int D>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chunk_kernel(const ChunkArgs) {
@@ -638,13 +639,13 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
       const int whole = wk.any_bad ? 0 : max(all_see - pc.from * kTileKeys, 0) / step;
       // Step t: at its barrier all waves' copies of it have landed (at most those of the two after it have
       // not), and the step before it has been read by all: step t + 3 takes its place.  (Nothing is
-      // written to LDS but by copies, and what was read has been used: no fence is needed, which would
-      // wait for all copies.)  With kEdge it may be seen in part.
+      // written to LDS but by copies: no fence is needed, which would wait for all of them.)  With kEdge it
+      // may be seen in part.
       int t = 0;
       auto turn = [&](const uint8_t* here, uint8_t* free, auto edge, int lane) __attribute__((always_inline)) {
         constexpr bool kEdge = decltype(edge)::value;
         asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(until_vmcnt(kEdge ? 0 : 2 * kCopies));
+        __builtin_amdgcn_s_waitcnt(until_read_and_vmcnt(kEdge ? 0 : 2 * kCopies));
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         if (!kEdge || t + 3 < steps) copy_next(free);
@@ -747,7 +748,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
 // a row: each such group of lanes a row of its own, or, of many parts, every kGroups-th part of the
 // workgroup's row.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinGroups = 8;   // workgroups of a part
+constexpr int kJoinGroups = 4;   // workgroups of a part (64 steps of 500 to 8100 positions: 109 us, with eight 112)
 constexpr int kJoinPerCu = 8;    // workgroups on a compute unit
 constexpr int kManyParts = 16;
 template <int D>
