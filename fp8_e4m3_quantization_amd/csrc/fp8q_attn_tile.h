@@ -136,13 +136,14 @@ struct RowSums {
         for (int r = 0; r < 16; ++r) o[i][r] *= f;
     }
     const float base = ref == neg_inf() ? 0.0f : ref;
-    if (kFused && __any(__builtin_fabsf(base) > kFar)) {
+    const bool is_far = __builtin_fabsf(base) > kFar;
+    if (kFused && __any(is_far)) {  // (rows that are not keep their bits)
       const float back = 1.0f / scale;
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[b][r] = (s[b][r] * scale - base) * back;
-      return 0.0f;
+        for (int r = 0; r < 16; ++r) s[b][r] = is_far ? (s[b][r] * scale - base) * back : s[b][r];
+      return is_far ? 0.0f : base;
     }
     return base;
   }

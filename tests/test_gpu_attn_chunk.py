@@ -370,3 +370,82 @@ def test_another_stream_and_two_replayed_graphs():
                 g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+def test_a_graph_replayed_over_growing_histories():
+    """Lengths, starts and tables are read at replay: the same graph serves step after step, whether its
+    histories are cut or not, and as many new tokens as the rows hold."""
+    s = _setup([2, 2, 60], [6000, 40, 900], 8, 2, 128, 16, extra=8, nan_behind=False)
+    for p in ("kc", "vc"):
+        s[p] = (s[p] & 0x77).contiguous()  # no NaN codes: stale positions become real ones
+    s["tables"] = s["tables"].contiguous()
+    tables, lens, cu = s["tables"].clone(), s["lens"].clone(), s["cu"].clone()
+    out, lse = torch.zeros_like(s["q"]), torch.zeros((64, 8), device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _call(s, out=out, lse=lse)
+    for step, starts in enumerate([[0, 2, 4, 64], [0, 1, 2, 3], [0, 0, 64, 64], [0, 2, 4, 64], [0, 0, 0, 0]]):
+        s["cu"].copy_(torch.tensor(starts))
+        s["lens"].copy_(torch.tensor([6000 - 2500 * step, 64 + step, 100 + 200 * step]).clamp(min=0))
+        s["tables"].copy_(tables.flip(0) if step == 3 else tables)
+        if step == 3:  # (the first row's blocks for the last sequence: the same ones, another order)
+            s["lens"].copy_(torch.tensor([0, 64, 6000]))
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        graph.replay()
+        eager, elog = torch.full_like(out, 7.0), torch.full_like(lse, 7.0)
+        _call(s, out=eager, lse=elog)
+        assert torch.equal(out, eager) and torch.equal(lse, elog), step
+        covered = _check(s, out, lse, some=[0, 1, 31, 32, 59, 63])
+        assert (out[~covered] == 7).all() and (lse[~covered] == 7).all()
+    s["lens"].copy_(lens)
+    s["cu"].copy_(cu)
+    s["tables"].copy_(tables)
+    graph.replay()
+    _check(s, out, lse, some=[0, 1, 59])
+
+
+@pytest.mark.parametrize("q_lens,lens", [([3, 4, 1, 70], [600, 640, 33, 700]), ([200, 2], [900, 901])])
+def test_blocks_shared_by_sequences_and_named_twice(q_lens, lens):
+    """A prefix that several sequences share, and one block that a table names again."""
+    s = _setup(q_lens, lens, 8, 2, 128, 16, nan_behind=False)
+    for p in ("kc", "vc"):
+        s[p] = (s[p] & 0x77).contiguous()
+    s["tables"] = s["tables"].clone()
+    s["tables"][1:, :2] = s["tables"][0, :2]
+    s["tables"][0, 5] = s["tables"][0, 4]
+    s["tables"][0, 6] = s["tables"][0, 0]
+    lse = torch.zeros((sum(q_lens), 8), device=DEV)
+    _check(s, _call(s, lse=lse), lse, some=[0, 1, 2, 3, 69, 127, 128, 199])
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("q_lens,lens", [([3], [2000]), ([40], [300]), ([100], [2000])])
+def test_a_query_that_is_not_finite_stays_alone(q_lens, lens, bad):
+    for d, hq, hkv in ((64, 8, 2), (128, 8, 8), (256, 4, 1)):
+        s = _setup(q_lens, lens, hq, hkv, d, 16)
+        clean = _call(s).view(-1, hq, d)
+        s["q"].view(-1, hq, d)[q_lens[0] // 2, hq - 1, 5] = bad
+        out = _call(s).view(-1, hq, d)
+        hit = torch.zeros((q_lens[0], hq), dtype=torch.bool, device=DEV)
+        hit[q_lens[0] // 2, hq - 1] = True
+        assert torch.equal(out[~hit], clean[~hit])
+        if math.isnan(bad):
+            assert torch.isnan(out[hit].float()).all()
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(64, 8, 8), (128, 16, 4), (256, 4, 4), (256, 8, 2), (128, 200, 1)])
+@pytest.mark.parametrize("q_lens,lens", [([3], [700]), ([7, 30], [2000, 90])])
+def test_nan_codes_of_heads_that_share_a_piece(d, hq, hkv, q_lens, lens):
+    s = _setup(q_lens, lens, hq, hkv, d, 16)
+    clean = _call(s).view(-1, hq, d)
+    pos, head, value = lens[0] - 2, hkv - 1, d - 3
+    s["vc"][int(s["tables"][0, pos // 16]) * s["cs"] + (pos % 16 * hkv + head) * d + value] = 0x7F
+    out = _call(s).view(-1, hq, d)
+    want = torch.zeros((sum(q_lens), hq, d), dtype=torch.bool, device=DEV)
+    want[q_lens[0] - 2:q_lens[0], head * (hq // hkv):, value] = True
+    assert torch.equal(torch.isnan(out.float()), want) and torch.equal(out[~want], clean[~want])
+
+
+def test_more_query_heads_than_a_tile_holds():
+    _run([1, 3, 9], [300, 3, 1000], 200, 1, 128, 16, some=[0, 2, 8])
