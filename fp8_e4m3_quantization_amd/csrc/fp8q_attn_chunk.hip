@@ -5,7 +5,32 @@
 // own among them), over the positions j that it sees (all of them, or causal j <= i + len - Lq):
 //   s_j = softmax_scale * k_scale * q . K_j
 //   out = v_scale * sum_j exp(s_j - r) V_j / sum_j exp(s_j - r),  lse = r + log sum_j exp(s_j - r)
-// for any reference r.  A query that sees no position gets zeros and lse = -infinity.
+// for any reference r.  A query that sees no position gets zeros and lse = -infinity.  Scores, sums and
+// statistics are binary32; the weights are rounded to bf16 for the second product, and out's
+// denominator sums the rounded ones, so that a weight above all others loses nothing by it.
+//
+// What bounds it: bytes where each position meets few queries (64 steps of 500 to 8100 positions,
+// 32/8 heads x 128: 109 us for 525 MB, 4.8 TB/s, where a copy reaches 5.1), the vector ALUs where it meets
+// many (512 tokens behind 8192, 40/4 heads x 128: 112 us; 44 % of the cycles the matrix cores and 67 % the
+// vector ALUs are busy, 88.7 GFLOP at 0.79 PFLOP/s): there each of a tile's four waves widens every code from
+// E4M3 to bf16 for itself, beside the exponentials.
+//
+// Layout.  A row is a query and a head of a KV head's group, so that grouped heads share what is read.  A
+// wave owns 32 rows: S^T = K Q^T leaves a row's scores in two lanes, where they are the second
+// product's operand (O^T = V^T P^T) as they lie.  Codes go global -> LDS by DMA, several steps ahead, and
+// are widened in registers as each wave reads them; V comes through the transposing LDS read.  (Widened
+// once a workgroup into bf16 tiles in LDS, the 512 tokens took 125 us when this took 123: half the
+// conversions, twice the LDS bytes and two more barriers.)
+//
+// Two forms.  Many rows: a workgroup takes 128 rows and steps of 64 positions, a row wave each; with 33 to 64
+// rows two waves, and the other two another KV head or every other step.  Up to 32 rows: each wave takes a KV
+// head, or every second or fourth block of 32 positions, in a part of LDS of its own without barriers, and
+// the waves of a head add up at the end.
+//
+// Work is cut into parts along the positions where the batch does not fill the GPU: every workgroup reads
+// all lengths, estimates the time of 64 ways to cut and takes the best (see find_limit); the parts'
+// sums go through the workspace to a second kernel that adds them up in their order.  No atomics: the
+// same bits every time.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -21,13 +46,19 @@ namespace {
 
 constexpr int kTileRows = 128;   // rows (query, head of a KV head's group) of a workgroup
 constexpr int kThreads = 256;
-constexpr int kSplitSeqs = 256;  // batches of more sequences are not split along the positions
-constexpr int kFewRows = 64;     // so many rows of a sequence and KV head at most: another form
-constexpr int kMinPart = 4;      // tiles of positions of a part, at least
+// Batches of more sequences are not split along the positions: they fill the GPU, and the estimate
+// goes over all of them in every workgroup.
+constexpr int kSplitSeqs = 256;
+// So many rows of a sequence and KV head at most: the waves divide heads and positions instead of rows.  64
+// sequences of 12 tokens (48 rows) over 500 to 8100 positions 141 us, as part of a tile of 128 rows 185; 64
+// steps (4 rows) 109, 172 there.
+constexpr int kFewRows = 64;
+constexpr int kMinPart = 4;      // tiles of positions of a part, at least (2 to 8: alike)
 constexpr int kMinFewPart = 1;   // the same of few rows
 // Times, in that of a tile of positions of a workgroup of many rows that shares its compute unit:
 constexpr float kFewCost = 0.8f;    // a tile of positions of few rows, for each KV head
-constexpr float kAloneCost = 0.6f;  // a tile of a workgroup alone on its compute unit
+constexpr float kAloneCost = 0.6f;  // a tile of a workgroup alone on its compute unit (as if 1: 16
+                                    // sequences of 4 tokens 32 -> 36 us)
 constexpr float kPieceCost = 2.0f;  // a workgroup's start and end
 constexpr float kJoinCost = 0.011f; // a part's sums, written and read again
 
@@ -77,7 +108,7 @@ struct Seq {
   // tiles of positions
   __device__ __forceinline__ int steps() const { return lq > 0 ? (len + kTileKeys - 1) / kTileKeys : 0; }
   // KV heads of a piece: a token's heads lie side by side in the pools, and one head's rows read
-  // alone stream slower
+  // alone stream slower (64 steps over 32/8 heads: 137 us of one head a piece, 116 of two, 109 of four)
   __device__ __forceinline__ int heads(const ChunkArgs& a) const {
     return few(a) ? min(a.most_heads, rows(a) > kWaveRows ? 2 : 4) : 1;
   }
@@ -383,6 +414,8 @@ __device__ __forceinline__ void copy16(const uint8_t* from, uint8_t* to) {
 constexpr int until_vmcnt(int n) { return (n & 15) | (n >> 4) << 14 | 0x0F70; }
 constexpr int until_read_and_vmcnt(int n) { return until_vmcnt(n) & ~0x0F00; }
 
+// Workgroups of a compute unit: as many as registers allow without spills in the loops (two 64-wide prompts: 90 us
+// at two, 87 at three, 97 at four).
 template <int D>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chunk_kernel(const ChunkArgs) {
   const ChunkArgs& a = own_args();
@@ -475,12 +508,14 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
 
   // A wave's rows over 32 kBlocks positions from p0 on, whose codes lie in LDS; with kEdge they may be
   // seen in part.
-  auto attend = [&](const uint8_t* ks, const uint8_t* vs, int p0, auto blocks, auto edge, int lane) __attribute__((always_inline)) {
+  auto attend = [&](const uint8_t* ks, const uint8_t* vs, int p0, auto blocks, auto edge,
+                    int lane) __attribute__((always_inline)) {
     constexpr int kBlocks = decltype(blocks)::value;
     constexpr bool kEdge = decltype(edge)::value;
     v16f s[kBlocks];
     code_scores<D, kBlocks>(s, ks, qf, lane);
-    // values are read before the weights are made, as registers allow
+    // values are read before the weights are made, as registers allow (512 behind 8192 113 us, after them 116;
+    // 256-wide heads 66 after them, before them 87: spills)
     constexpr int kSteps = 2 * kBlocks, kEarly = D == 256 ? 0 : kSteps;
     v2u y[kSteps][D / 32];
     auto read_values = [&](int st) {
@@ -580,7 +615,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
     // waves each go over.
     auto go = [&](auto blocks) __attribute__((always_inline)) {
       constexpr int kBlocks = decltype(blocks)::value;
-      constexpr int kRows = kBlocks == 2 ? D / 64 : D / 32;   // rows that a lane copies, of keys and values or of either
+      // rows that a lane copies, of keys and values or of either
+      constexpr int kRows = kBlocks == 2 ? D / 64 : D / 32;
       constexpr int kCopies = D / 32;                         // copies of a wave and step
       typedef Rows<D, kRows> R;
       const int lane = own_lane();
@@ -750,7 +786,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
 constexpr int kJoinThreads = 256;
 constexpr int kJoinGroups = 4;   // workgroups of a part (64 steps of 500 to 8100 positions: 109 us, with eight 112)
 constexpr int kJoinPerCu = 8;    // workgroups on a compute unit
-constexpr int kManyParts = 16;
+constexpr int kManyParts = 16;   // (4 sequences of 1 and 4 tokens, 256-wide heads: 28 us, as if few 36; two
+                                 // 64-wide prompts 87, as if many 132)
 template <int D>
 __global__ __launch_bounds__(kJoinThreads) void chunk_join_kernel(const ChunkArgs a) {
   constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
@@ -840,6 +877,8 @@ ChunkPlan chunk_plan(int32_t seqs, int32_t tq, int32_t hq, int32_t hkv, int32_t 
   const int64_t some = seqs < tq ? seqs : tq;  // sequences that have a query
   p.pieces = (rows + some * (kTileRows - 1)) / kTileRows + 2;  // (lists that are dealt to: one more each)
   p.resident = float(num_cus() * (d == 256 ? 1 : d == 128 ? 2 : 3)) / float(hkv);
+  // (room for the pieces that run at once: 64-wide prompts 105 us instead of 87; for three times as many:
+  // 1 x 5 tokens 16.9 -> 17.8, the more workgroups that find nothing to do)
   const int slots = int(1.75f * p.resident);
   // (with whole tiles for all slots nothing is split)
   if (seqs <= kSplitSeqs && slots > 3 && rows / kTileRows < slots) p.slots = slots;

@@ -11,6 +11,12 @@
 //
 // Eight lanes take a group, 16 values each, as in fp8_group_quant: two 16-byte loads of each input,
 // one 16-byte store of codes, the maximum over eight lanes without LDS.
+//
+// What bounds them: memory for many rows (4593 x 5120 with a residual: 34.3 us, 165 MB at 4.8 TB/s, 94 % of a
+// copy's rate; 4593 x 16384 of gate and up: 63.7 us, 379 MB at 5.9 TB/s, reads outweighing writes), the
+// host's call for few (16 x 5120: 7.3 us, 3.8 on the GPU; 16 x 16384 of gate and up 6.4 and 4.1).  A row is a
+// workgroup's, so that its squares' sum needs one barrier and its values stay in registers; a workgroup
+// that goes on to further rows instead of ending took 37.9 us for the 34.6 of then.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -217,7 +223,7 @@ struct SiluArgs {
   FastDiv per_row;  // groups of a row
 };
 
-constexpr int kSiluBlock = 512;
+constexpr int kSiluBlock = 512;  // (256 and 1024 threads: within 2 %)
 constexpr int kSiluGroups = kSiluBlock / 8;
 
 __global__ __launch_bounds__(kSiluBlock) void silu_kernel(const SiluArgs a) {
