@@ -162,6 +162,24 @@ def test_many_sequences(seqs):
     _run(q_lens, [max(q, (i * 53) % 190) for i, q in enumerate(q_lens)], 4, 2, 64, 16)
 
 
+@pytest.mark.parametrize("seqs", [100, 260])
+@pytest.mark.parametrize("hq,hkv", [(4, 4), (6, 6), (3, 3)])
+@pytest.mark.parametrize("rows", [[129], [32, 33], [65, 1], [128, 129, 64, 257]])
+def test_many_sequences_whose_tiles_are_barely_begun(seqs, hq, hkv, rows):
+    """As many pieces as rows of such numbers can make: each finds a workgroup."""
+    q_lens = [rows[i % len(rows)] for i in range(seqs)]
+    s = _setup(q_lens, [q + i % 3 for i, q in enumerate(q_lens)], hq, hkv, 64, 16)
+    out = torch.full_like(s["q"], math.nan)
+    lse = torch.full((sum(q_lens), hq), math.nan, device=DEV)
+    _call(s, out=out, lse=lse)
+    assert not torch.isnan(out).any() and not torch.isnan(lse).any()
+    some = [s["cu"][i].item() for i in (0, 1, seqs - 1)]
+    for i, at in zip((0, 1, seqs - 1), some):
+        one = dict(s, q=s["q"][at:at + q_lens[i]].contiguous(), tables=s["tables"][i:i + 1].contiguous(),
+                   lens=s["lens"][i:i + 1], cu=torch.tensor([0, q_lens[i]], dtype=torch.int32, device=DEV))
+        _check(one, out[at:at + q_lens[i]], lse[at:at + q_lens[i]])
+
+
 def test_a_serving_batch():
     """One chunk beside single steps and a whole prompt, wide tables, strides, rows behind the last."""
     q_lens, lens = [1] * 12 + [200, 1, 90], [40 + 300 * i for i in range(12)] + [1900, 5, 90]
