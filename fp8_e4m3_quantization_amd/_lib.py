@@ -917,6 +917,8 @@ def fp8_attn_chunk(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         raise ValueError("block_tables must be [num_seqs, max_blocks], context_lens [num_seqs], "
                          "cu_seqlens_q [num_seqs + 1]")
     width = block_tables.shape[1]
+    if width > 0x7FFFFFFF:
+        raise ValueError(f"block_tables of {width} columns are too wide")
     table_stride, inner = block_tables.stride()
     if inner != 1 and width > 1:
         raise ValueError("block_tables' rows must be packed")
@@ -960,6 +962,8 @@ def _rows(t: torch.Tensor, name: str, like: tuple | None = None):
 def _group_outputs(shape, q, scales, device, stream):
     """Codes and scales for rows of this shape, allocated where not given."""
     m, k = shape
+    if k > 0x7FFFFFFF:
+        raise ValueError(f"{k} columns are too many")
     if q is None or scales is None:
         with _on_stream(stream, device):
             if q is None:

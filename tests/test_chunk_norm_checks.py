@@ -126,6 +126,8 @@ def test_binding_refuses_chunk_shapes():
         call(q, pool, pool, tab, lens, cu, out=q, lse=torch.zeros((8, 9)))
     with pytest.raises(ValueError, match="rows must be packed"):
         call(q, pool, pool, torch.zeros((3, 8), dtype=torch.int32)[:, ::2], lens, cu)
+    with pytest.raises(ValueError, match="too wide"):  # (32 bits of it would pass for a width of 4)
+        call(q, pool, pool, torch.empty((3, (1 << 32) + 4), dtype=torch.int32, device="meta"), lens, cu)
     with pytest.raises(ValueError, match="GPU memory"):
         call(q, pool, pool, tab, lens, cu)
 
@@ -153,6 +155,10 @@ def test_binding_refuses_norm_and_silu_shapes():
         silu(x, x[:, :128])
     with pytest.raises(ValueError, match="out must be"):
         silu(x, x, out=x[:2])
+    wide = torch.empty((1, (1 << 32) + 128), dtype=BF16, device="meta")
+    for call in (lambda: norm(wide, None), lambda: silu(wide, wide)):
+        with pytest.raises(ValueError, match="too many"):
+            call()
     for call in (lambda: norm(x, w), lambda: silu(x, x)):
         with pytest.raises(ValueError, match="GPU memory"):
             call()
