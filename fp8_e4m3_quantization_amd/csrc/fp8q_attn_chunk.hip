@@ -49,6 +49,10 @@ constexpr int kThreads = 256;
 // Batches of more sequences are not split along the positions: they fill the GPU, and the estimate
 // goes over all of them in every workgroup.
 constexpr int kSplitSeqs = 256;
+// Nor are those whose tables have room for so many positions at most, which one kernel is faster for: 200
+// positions of 1, 5, 37 and 200 tokens, 40/4 heads: 12.7, 14.2, 13.4 and 12.2 us whole, 13.3, 14.9, 16.8 and 15.6
+// with parts and their join; 400 positions: 17.4, 18.8, 16.8, 17.1 and 13.6, 15.7, 20.3, 20.3.
+constexpr int kShort = 256;
 // So many rows of a sequence and KV head at most: the waves divide heads and positions instead of rows.  64
 // sequences of 12 tokens (48 rows) over 500 to 8100 positions 141 us, as part of a tile of 128 rows 185; 64
 // steps (4 rows) 109, 172 there.
@@ -868,7 +872,8 @@ int chunk_shape(int32_t seqs, int32_t tq, int32_t hq, int32_t hkv, int32_t d) {
 struct ChunkPlan {
   int slots;       // pieces of a KV head when sequences are split; 0: they are not
   float resident;  // pieces of a KV head that run at once
-  int64_t pieces;  // that a KV head may have
+  int64_t whole;   // pieces that a KV head may have, when sequences are not split
+  int64_t pieces;  // and when they are
   uint64_t sums_bytes, stats_bytes, bytes;
 };
 // KV heads that a piece of few rows takes at most.
@@ -883,16 +888,16 @@ ChunkPlan chunk_plan(int32_t seqs, int32_t tq, int32_t hq, int32_t hkv, int32_t 
   // Workgroups that find nothing read all lengths for it: by the first bound alone 1024 steps of 100 to 1700
   // positions take 420 us instead of 367, 8192 of 1 to 64 positions 7.3 ms instead of 1.7.
   const int64_t heads = most_heads(hkv);
-  p.pieces = (rows + some * (kTileRows - 1)) / kTileRows + 2;
+  p.whole = (rows + some * (kTileRows - 1)) / kTileRows + 2;
   const int64_t shared = (some + (2 * heads - 1) * rows / (kTileRows + 1)) / heads + 4;
-  if (heads > 1 && shared < p.pieces) p.pieces = shared;
+  if (heads > 1 && shared < p.whole) p.whole = shared;
   p.resident = float(num_cus() * (d == 256 ? 1 : d == 128 ? 2 : 3)) / float(hkv);
   // (room for the pieces that run at once: 64-wide prompts 105 us instead of 87; for three times as many:
   // 1 x 5 tokens 16.9 -> 17.8, the more workgroups that find nothing to do)
   const int slots = int(1.75f * p.resident);
   // (with whole tiles for all slots nothing is split)
   if (seqs <= kSplitSeqs && slots > 3 && rows / kTileRows < slots) p.slots = slots;
-  if (p.slots > p.pieces) p.pieces = p.slots;
+  p.pieces = p.slots > p.whole ? p.slots : p.whole;
   if (p.slots == 0) return p;
   const uint64_t all = uint64_t(p.slots) * hkv * kTileRows;
   p.sums_bytes = all * d * 4;
@@ -956,11 +961,12 @@ extern "C" int fp8_attn_chunk(const uint16_t* q, const uint8_t* k_cache, const u
     if (!aligned(workspace, 256)) return FP8Q_EALIGN;
     if (workspace_bytes < p.bytes) return FP8Q_EINVAL;
   }
+  const bool cut = p.slots > 0 && int64_t(max_blocks) * block_size > kShort;
   ChunkArgs a = {};
   a.q = q, a.kc = k_cache, a.vc = v_cache, a.tables = block_tables, a.lens = context_lens;
   a.cu = cu_seqlens_q, a.out = out, a.lse = lse;
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
-  if (p.slots > 0) {
+  if (cut) {
     a.sums = reinterpret_cast<float*>(ws);
     a.stats = reinterpret_cast<float4*>(ws + p.sums_bytes);
     a.parts = reinterpret_cast<int4*>(ws + p.sums_bytes + p.stats_bytes);
@@ -970,14 +976,15 @@ extern "C" int fp8_attn_chunk(const uint16_t* q, const uint8_t* k_cache, const u
   a.group = num_q_heads / num_kv_heads, a.bs = block_size, a.causal = causal != 0;
   a.by_group = FastDiv(uint32_t(a.group)), a.by_block = FastDiv(uint32_t(block_size));
   a.most_heads = most_heads(num_kv_heads);
-  a.slots = p.slots, a.resident = p.resident, a.scale_log2 = softmax_scale * k_scale * kLog2e, a.v_scale = v_scale;
+  a.slots = cut ? p.slots : 0, a.resident = p.resident, a.scale_log2 = softmax_scale * k_scale * kLog2e, a.v_scale = v_scale;
   const int64_t per = num_kv_heads % 8 == 0 ? 8 : 8 % num_kv_heads == 0 ? 8 / num_kv_heads : 1;
-  const int64_t blocks = num_kv_heads % 8 == 0 ? p.pieces * num_kv_heads
-                                               : (p.pieces + per - 1) / per * per * num_kv_heads;
+  const int64_t pieces = cut ? p.pieces : p.whole;
+  const int64_t blocks = num_kv_heads % 8 == 0 ? pieces * num_kv_heads
+                                               : (pieces + per - 1) / per * per * num_kv_heads;
   if (blocks > 0x7FFFFFFF) return FP8Q_EINVAL;
   auto kern = head_dim == 64 ? chunk_kernel<64> : head_dim == 128 ? chunk_kernel<128> : chunk_kernel<256>;
   launch(kern, dim3(unsigned(blocks)), dim3(kThreads), 0, stream, a);
-  if (launch_status() != FP8Q_OK || p.slots == 0) return launch_status();
+  if (launch_status() != FP8Q_OK || !cut) return launch_status();
   auto join = head_dim == 64 ? chunk_join_kernel<64>
               : head_dim == 128 ? chunk_join_kernel<128> : chunk_join_kernel<256>;
   const int joins = p.slots * num_kv_heads * kJoinGroups, most = kJoinPerCu * num_cus();

@@ -546,7 +546,9 @@ int fp8_attn_decode(const uint16_t* q, const uint8_t* k_cache, const uint8_t* v_
  * The scores must stay within binary32.  Outputs must not overlap inputs.
  * Where the batch is too small to fill the GPU by its queries alone, histories are cut into parts:
  * then a workspace is needed and two kernels are enqueued, the second joining the parts in order
- * (batches of more than 256 sequences are never cut).
+ * (batches of more than 256 sequences are never cut, nor those whose tables have room for at most
+ * 256 positions, though the workspace is checked: a table no wider than needed is the faster one for
+ * short histories).
  * fp8_attn_chunk_workspace_size: for the current device.
  * Errors: FP8Q_EINVAL, FP8Q_ENULL, FP8Q_EALIGN, FP8Q_ELAUNCH. */
 int fp8_attn_chunk_workspace_size(int32_t num_seqs, int32_t total_q, int32_t num_q_heads,

@@ -152,6 +152,13 @@ def test_whole_prompts_and_a_step_agree_with_the_other_kernels():
     assert ((step.float() - out.float()).abs() <= 2.0 ** -6 * out.float().abs() + 0.02).all()
 
 
+@pytest.mark.parametrize("extra", [0, 1, 40])
+@pytest.mark.parametrize("q_lens,lens", [([1], [256]), ([37], [255]), ([5, 1, 2], [256, 17, 250]), ([200], [256])])
+def test_short_tables_and_wide_ones(q_lens, lens, extra):
+    """Tables with room for 256 positions, one block more, and many: one kernel or two."""
+    _run(q_lens, lens, 8, 2, 128, 16, extra=extra)
+
+
 def test_chunks_without_a_causal_mask():
     _run([5, 40, 1, 200], [300, 40, 7, 250], 8, 2, 128, 16, causal=False)
 
