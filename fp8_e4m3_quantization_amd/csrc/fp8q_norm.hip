@@ -190,19 +190,20 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
 }
 
 // Rows longer than that: read twice, the second time as stored where a residual was added.  A lane
-// reads again what it wrote itself.
+// reads again what it wrote itself.  Columns count in 32 bits without a sign: behind the last ones of rows of
+// nearly 2^31 values lies a column past 2^31.
 __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a) {
-  const int step = blockDim.x * kLaneValues;
+  const uint32_t step = blockDim.x * kLaneValues, k = a.k;
   int parity = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
     float sq = 0.0f;
-    for (int c = threadIdx.x * kLaneValues; c < a.k; c += step) {
+    for (uint32_t c = threadIdx.x * kLaneValues; c < k; c += step) {
       uint4 h[2];
       load_sum(a, row, c, h);
       sq += sq_sum16(h);
     }
     const float r = rsqrtf(sum_over_group(sq, parity) / float(a.k) + a.eps);
-    for (int c = threadIdx.x * kLaneValues; c < a.k; c += step) {
+    for (uint32_t c = threadIdx.x * kLaneValues; c < k; c += step) {
       uint4 h[2], w[2];
       const uint16_t* from = a.residual ? a.sum + row * a.ss + c : a.x + row * a.xs + c;
       h[0] = *reinterpret_cast<const uint4*>(from);
