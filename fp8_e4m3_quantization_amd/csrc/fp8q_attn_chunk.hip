@@ -976,7 +976,10 @@ extern "C" int fp8_attn_chunk(const uint16_t* q, const uint8_t* k_cache, const u
   a.group = num_q_heads / num_kv_heads, a.bs = block_size, a.causal = causal != 0;
   a.by_group = FastDiv(uint32_t(a.group)), a.by_block = FastDiv(uint32_t(block_size));
   a.most_heads = most_heads(num_kv_heads);
-  a.slots = cut ? p.slots : 0, a.resident = p.resident, a.scale_log2 = softmax_scale * k_scale * kLog2e, a.v_scale = v_scale;
+  a.slots = cut ? p.slots : 0, a.resident = p.resident, a.v_scale = v_scale;
+  // Masked scores are -infinity before they are scaled, and a scale of 0 would make them NaN: where the product
+  // leaves binary32 it is its smallest number, which takes the largest score below 2^-21, the weight 1.
+  a.scale_log2 = fmaxf(softmax_scale * k_scale * kLog2e, 0x1p-149f);
   const int64_t per = num_kv_heads % 8 == 0 ? 8 : 8 % num_kv_heads == 0 ? 8 / num_kv_heads : 1;
   const int64_t pieces = cut ? p.pieces : p.whole;
   const int64_t blocks = num_kv_heads % 8 == 0 ? pieces * num_kv_heads

@@ -1,9 +1,13 @@
 """GPU: the ends of what fp8_rms_norm_group_quant, fp8_silu_mul_group_quant and fp8_attn_chunk accept."""
+import math
+
 import pytest
 import torch
 
 import fp8_e4m3_quantization_amd as fq
+from tests import attn_ref
 from tests.gpu_util import DEV, need_gpu
+from tests.test_gpu_attn_chunk import _setup
 
 pytestmark = pytest.mark.gpu
 BF16, F64 = torch.bfloat16, torch.float64
@@ -37,3 +41,39 @@ def test_norm_of_one_row_of_nearly_two_to_the_31_columns(k):
     for i in range(0, k // 128 - 1, 1 << 20):
         part = rows[i:min(i + (1 << 20), k // 128 - 1)]
         assert (part == codes).all(), i
+
+
+@pytest.mark.parametrize("k_scale,scale", [(2.0 ** -64, 2.0 ** -149), (2.0 ** -64, 2.0 ** -100), (2.0 ** -64, 1e-30),
+                                           (2.0 ** -64, 2.0 ** -86), (2.0 ** -64, 2.0 ** -70), (1.0, 2.0 ** -149)])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 8, 2), (128, 4, 4), (256, 4, 1)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_chunk_of_the_smallest_scales(k_scale, scale, d, hq, hkv, causal):
+    """Scores next to 0, be their scale's product below binary32's smallest number: out is the mean of V over the
+    positions that a query sees, off by its own rounding and the sums' (n + 8) steps; lse the logarithm of their
+    number.  With queries of 2^98 the scores reach 2^112 before a scale of at most 2^-134: weights off by
+    2^-21 at most."""
+    q_lens, lens = [1, 3, 40, 130, 5], [1, 700, 40, 300, 5000]
+    s = _setup(q_lens, lens, hq, hkv, d, 16)
+    s["tables"] = s["tables"].clone()
+    s["tables"][3, 4] = -1
+    nb = s["kc"].numel() // s["cs"]
+    vp = s["vc"].view(nb, 16, hkv, d)
+    for q in (s["q"], (s["q"].float() * 2.0 ** 96).to(BF16)):
+        lse = torch.zeros((sum(q_lens), hq), device=DEV)
+        out = fq.fp8_attn_chunk(q, s["kc"], s["vc"], s["tables"], s["lens"], s["cu"], hq, hkv, d, 16, k_scale, 0.5,
+                                softmax_scale=scale, causal=causal, lse=lse)
+        first = 0
+        for i, (lq, n) in enumerate(zip(q_lens, lens)):
+            pos = torch.arange(n, device=DEV)
+            ids = s["tables"][i].long()[pos // 16]
+            good = ids >= 0
+            seen = attn_ref.causal_mask(lq, n, DEV) if causal else torch.ones((lq, n), dtype=torch.bool, device=DEV)
+            w = seen[:, good].to(F64)
+            w /= w.sum(1, keepdim=True)
+            for h in range(hq):
+                v = 0.5 * attn_ref.e4m3_values(vp[ids[good], (pos % 16)[good], h // (hq // hkv)])
+                bound = attn_ref.HALF_BF16 * (w @ v).abs() + ((n + 8) * U24 + 2.0 ** -20) * (w @ v.abs())
+                attn_ref.check(out[first:first + lq].view(lq, hq, d)[:, h], w @ v, bound, f"sequence {i} out")
+            want = torch.log(seen[:, good].sum(1).to(F64))[:, None].expand(lq, hq)
+            attn_ref.check(lse[first:first + lq], want, 5 * U24 * want.abs() + 2.0 ** -20, f"sequence {i} lse")
+            first += lq
