@@ -255,7 +255,7 @@ __global__ __launch_bounds__(kSiluBlock) void silu_kernel(const SiluArgs a) {
 
 // What both calls check of their rows: k whole groups, fewer than 2^31 groups, strides.
 bool rows_ok(int64_t m, int32_t k) {
-  return m >= 0 && k > 0 && k % 128 == 0 && m <= (int64_t(1) << 31) / (k / 128) - 1;
+  return m >= 0 && k > 0 && k % 128 == 0 && m <= ((int64_t(1) << 31) - 1) / (k / 128);
 }
 bool stride_ok(int64_t stride, int32_t k) { return stride >= k && stride <= (int64_t(1) << 40); }
 
