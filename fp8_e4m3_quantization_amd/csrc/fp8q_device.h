@@ -99,8 +99,8 @@ __device__ __forceinline__ uint2 dequant4(uint32_t w, float s) {
   return make_uint2(pack_bf16x2(a.x * s, a.y * s), pack_bf16x2(b.x * s, b.y * s));
 }
 
-// Two binary32 -> two bf16 (round to nearest even) in one v_cvt_pk_bf16_f32; used only on
-// finite values (a NaN's bits are whatever the converter makes of it).
+// Two binary32 -> two bf16 (round to nearest even) in one v_cvt_pk_bf16_f32.  Infinities stay, finite
+// values beyond bf16's become infinite, and a NaN stays a NaN, whose other bits are the converter's choice.
 __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
   typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
   typedef float f32x2_t __attribute__((ext_vector_type(2)));

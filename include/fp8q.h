@@ -109,7 +109,8 @@ int fp8_group_quant(const uint16_t* x, uint8_t* q, float* scales, int64_t m, int
  *   q       device uint8 [m, k], 16-byte aligned;  scales  device fp32 [m, k/128]
  *   k > 0 and k % 128 == 0; m >= 0 (0 is a no-op), m * (k/128) < 2^31; 0 <= eps <= 1
  * The squares' sum must stay within binary32.  A NaN makes its row NaN codes; so does a row of
- * zeros with eps = 0.  Other outputs must not overlap inputs.
+ * zeros with eps = 0.  An infinity (of h: also a sum that rounds to one) makes its own value NaN
+ * and the others of its row 0.  Other outputs must not overlap inputs.
  * Errors: FP8Q_EINVAL, FP8Q_ENULL, FP8Q_EALIGN, FP8Q_ELAUNCH. */
 int fp8_rms_norm_group_quant(const uint16_t* x, const uint16_t* residual, const uint16_t* weight,
                              float eps, uint16_t* residual_out, uint16_t* norm_out, uint8_t* q,

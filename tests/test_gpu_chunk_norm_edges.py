@@ -77,3 +77,32 @@ def test_chunk_of_the_smallest_scales(k_scale, scale, d, hq, hkv, causal):
             want = torch.log(seen[:, good].sum(1).to(F64))[:, None].expand(lq, hq)
             attn_ref.check(lse[first:first + lq], want, 5 * U24 * want.abs() + 2.0 ** -20, f"sequence {i} lse")
             first += lq
+
+
+@pytest.mark.parametrize("k", [512, 5120, 16384, 40960])
+@pytest.mark.parametrize("place", ["new", "x", "residual"])
+def test_norm_of_sums_that_are_not_finite(k, place):
+    """A NaN or an infinity from x, from the residual, of both or of their sum's rounding to bf16: the sum is kept as
+    torch has it; a NaN makes its row NaN codes, an infinity its own value NaN and the row's others 0."""
+    g = torch.Generator(device=DEV).manual_seed(k)
+    x, r = (torch.randn((9, k), generator=g, device=DEV).to(BF16) for _ in range(2))
+    w = (torch.rand(k, generator=g, device=DEV) + 0.5).to(BF16)
+    big = torch.finfo(BF16).max
+    at = k - 7
+    for row, (a, b) in enumerate([(math.nan, 1.0), (1.0, math.nan), (math.inf, 1.0), (1.0, -math.inf),
+                                  (math.inf, -math.inf), (big, 2.0 ** 119), (-big, -big), (math.inf, math.nan)]):
+        x[row, at], r[row, at] = a, b
+    want = (x.float() + r.float()).to(BF16)
+    assert torch.isnan(want[[0, 1, 4, 7], at]).all() and torch.isinf(want[[2, 3, 5, 6], at]).all()
+    clean = fq.fp8_rms_norm_group_quant(x[8:], w, residual=r[8:])
+    to = {"new": None, "x": x, "residual": r}[place]
+    kept = torch.zeros_like(x)
+    q, s, total = fq.fp8_rms_norm_group_quant(x, w, residual=r, residual_out=to, norm_out=kept)
+    nan = torch.isnan(want)
+    assert torch.equal(torch.isnan(total), nan) and torch.equal(total[~nan], want[~nan])
+    codes = q & 0x7F
+    assert (codes[[0, 1, 4, 7]] == 0x7F).all()
+    for row in (2, 3, 5, 6):
+        assert codes[row, at] == 0x7F and int((codes[row] != 0).sum()) == 1, row
+    assert torch.equal(torch.isnan(kept), codes == 0x7F)
+    assert torch.equal(q[8:], clean[0]) and torch.equal(s[8:], clean[1])
