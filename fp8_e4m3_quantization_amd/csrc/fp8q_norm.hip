@@ -7,7 +7,8 @@
 //   silu:  y = gate / (1 + exp(-gate)) * up
 // and per group of 128 of the row: s = max(max|y|, 1e-10) / 448, codes = E4M3(y / s).  h is what
 // the layer keeps, so it is rounded first and normed as kept; y is not rounded before it is
-// quantized.  The quotient is a binary32 division's: reciprocal and one remainder correction.
+// quantized.  The quotient is a binary32 division's: reciprocal and one remainder correction (see
+// fp8q_math.h, which has that for binary32 dividends too).
 //
 // Eight lanes take a group, 16 values each, as in fp8_group_quant: two 16-byte loads of each input,
 // one 16-byte store of codes, the maximum over eight lanes without LDS.
