@@ -314,6 +314,7 @@ template <int D>
 struct Work {
   Piece pc;
   int kvh;
+  int wave_end;    // positions [0, wave_end) are seen by some row of the wave
   bool any_bad;    // some position of the piece lies in a block that does not exist
 
   // A position's block (behind the last position: the last one's).
@@ -321,10 +322,17 @@ struct Work {
     return a.tables[pc.seq * a.ts + a.by_block.div(min(pos, pc.len - 1))];
   }
   // Scores of positions that a row does not see, or that lie in blocks that do not exist, are
-  // -infinity; s holds positions p0 .. p0 + 32 kBlocks - 1.
+  // -infinity; s holds positions p0 .. p0 + 32 kBlocks - 1.  Returns a bit for each of the lane's positions that some
+  // row of the wave sees: NaN codes of the others' values (stale ones behind a sequence's end, those of a block in
+  // the place of one that does not exist) do not count, nor do they start take_nans, which goes over positions one
+  // by one (64 steps of 500 to 8100 positions behind a block that does not exist, stale codes NaN: 2850 us with it, 184 without).
   template <int kBlocks>
-  __device__ __forceinline__ void mask(v16f* s, int p0, int limit) const {
+  __device__ __forceinline__ uint32_t mask(v16f* s, int p0, int limit) const {
     const int half = (threadIdx.x & 63) >> 5, left = limit - p0 - 4 * half;
+    // (of every eight positions the lane has four)
+    const int any_left = wave_end - p0 - 4 * half;
+    const int n = min(max(4 * (any_left >> 3) + min(any_left & 7, 4), 0), 16 * kBlocks);
+    uint32_t counts = uint32_t((uint64_t(1) << n) - 1);
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
@@ -344,7 +352,9 @@ struct Work {
       for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[b][r] = good >> (16 * b + r) & 1 ? s[b][r] : neg_inf();
+      counts &= good;
     }
+    return counts;
   }
   // NaN codes that were left out of positions from `first` on reach a row that sees them.
   __device__ __forceinline__ void take_nans(RowSums<D>& sums, int first, int limit) const {
@@ -475,8 +485,10 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
   if (pc.parts > 1 && tid == 0)
     a.parts[pc.slot] = make_int4(pc.q0, pc.row0, pc.rows | row_waves << 8 | pc.heads << 12 | pc.kvh << 16,
                                  pc.part | pc.parts << 16);
-  Work<D> wk{pc, kvh, false};
   auto query_of = [&](int r) { return int(a.by_group.div(pc.row0 + r)); };
+  // (later queries see more)
+  const int wave_end = mine < pc.rows ? pc.seen(a, query_of(min(mine + kWaveRows, pc.rows) - 1)) : 0;
+  Work<D> wk{pc, kvh, __builtin_amdgcn_readfirstlane(wave_end), false};
   const int my_row = min(row, pc.rows - 1), my_query = query_of(my_row);
   const int my_head = kvh * a.group + pc.row0 + my_row - my_query * a.group;
   const int limit = row < pc.rows ? pc.seen(a, my_query) : 0;
@@ -508,7 +520,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
   RowSums<D> sums;
   sums.clear();
   const float scale = a.scale_log2;
-  uint32_t odd = 0;  // not 0: NaN codes of values were left out, at positions from first_left_out on
+  uint32_t odd = 0;  // not 0: NaN codes of values were left out that some row sees, from first_left_out on
   int first_left_out = pc.from * kTileKeys;
   const uint8_t* const kc = a.kc + int64_t(kvh) * D;
   const uint8_t* const vc = a.vc + int64_t(kvh) * D;
@@ -531,13 +543,14 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void chu
     };
 #pragma unroll
     for (int st = 0; st < kEarly; ++st) read_values(st);
-    if constexpr (kEdge) wk.template mask<kBlocks>(s, p0, limit);
+    uint32_t counts = 0;
+    if constexpr (kEdge) counts = wk.template mask<kBlocks>(s, p0, limit);
     v8bf p[kSteps];
     sums.template weigh<kBlocks>(s, scale, p);
 #pragma unroll
     for (int st = 0; st < kSteps; ++st) {
       if (st >= kEarly) read_values(st);
-      sums.template add_values<kEdge>(y[st], p[st], &odd);
+      sums.template add_values<kEdge>(y[st], p[st], counts >> (8 * st), &odd);
     }
   };
 

@@ -78,7 +78,7 @@ __device__ __forceinline__ v2u value_codes(const uint8_t* vs, int st, int i, int
       (lds_v2i*)(vs + (16 * st + r) * D + ((2 * i + side) ^ value_turn<D>(r)) * 16 + 8 * (i16 & 1))));
 }
 
-// NaN codes of w become 0; `odd` is not 0 where there were any.
+// NaN codes of w become 0; their bytes' top bits are added to `odd`.
 __device__ __forceinline__ uint32_t without_nans(uint32_t w, uint32_t* odd) {
   const uint32_t nan = e4m3_nan_bytes(w);
   *odd |= nan;
@@ -177,20 +177,23 @@ struct RowSums {
     const float base = move_to<kBlocks>(largest_score<kBlocks>(s) * scale, s, scale);
     sum += weights_of<kBlocks>(s, scale, base, p);
   }
-  // o^T += V^T P^T over 16 keys, whose values' codes are y.  With kClean NaN codes are left out (and
-  // `odd` tells).
+  // o^T += V^T P^T over 16 keys, whose values' codes are y.  With kClean NaN codes are left out, and
+  // `odd` tells of those of the keys that count (one bit for each of the lane's eight).
   template <bool kClean>
-  __device__ __forceinline__ void add_values(const v2u* y, v8bf p, uint32_t* odd) {
+  __device__ __forceinline__ void add_values(const v2u* y, v8bf p, uint32_t counts, uint32_t* odd) {
     const v4s ones = {0x3F80, 0x3F80, 0x3F80, 0x3F80};
     const v4u w = __builtin_bit_cast(v4u, p);
     rounded = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(ones, __builtin_bit_cast(v4s, v2u{w[0], w[1]}), rounded, 0, 0, 0);
     rounded = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(ones, __builtin_bit_cast(v4s, v2u{w[2], w[3]}), rounded, 0, 0, 0);
+    uint32_t odd0 = 0, odd1 = 0;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       v2u c = y[i];
-      if (kClean) c = v2u{without_nans(c[0], odd), without_nans(c[1], odd)};
+      if (kClean) c = v2u{without_nans(c[0], &odd0), without_nans(c[1], &odd1)};
       o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_bf16(c[0], c[1]), p, o[i], 0, 0, 0);
     }
+    // (four bits times this product: bit k is bit 8 k + 7, and others that no NaN code sets)
+    if (kClean) *odd |= (odd0 & ((counts & 15) * 0x10204080u)) | (odd1 & ((counts >> 4 & 15) * 0x10204080u));
   }
 };
 

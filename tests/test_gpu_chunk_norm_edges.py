@@ -106,3 +106,68 @@ def test_norm_of_sums_that_are_not_finite(k, place):
         assert codes[row, at] == 0x7F and int((codes[row] != 0).sum()) == 1, row
     assert torch.equal(torch.isnan(kept), codes == 0x7F)
     assert torch.equal(q[8:], clean[0]) and torch.equal(s[8:], clean[1])
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(64, 8, 2), (128, 8, 2), (256, 4, 2)])
+@pytest.mark.parametrize("q_lens,lens", [([2], [150]), ([14], [150]), ([70], [150]), ([3, 30], [2000, 130])])
+@pytest.mark.parametrize("gone", [False, True])
+def test_a_nan_code_at_every_position_of_the_last_tiles(d, hq, hkv, q_lens, lens, gone):
+    """One NaN code of a value at a time, at each of the last positions and behind the end: it reaches that value of the
+    rows that see it and nothing else, also where a block does not exist (and the NaN codes of the pool's
+    first block, read in its place, do not count)."""
+    s = _setup(q_lens, lens, hq, hkv, d, 16)
+    for p in ("kc", "vc"):
+        s[p] = torch.where(s[p] & 0x7F == 0x7F, 0x31, s[p]).contiguous()
+    if gone:
+        s["tables"] = s["tables"].clone()
+        used = s["tables"][0, 1].item()
+        s["tables"][0, 1] = -1
+        s["vc"][used * s["cs"]:(used + 1) * s["cs"]] = 0x7F
+        blocks = [x for b, n in enumerate(lens) for x in s["tables"][b, :-(-n // 16)].tolist()]
+        if 0 not in blocks:
+            s["vc"][:s["cs"]] = 0xFF
+    args = (s["q"], s["kc"], s["vc"], s["tables"], s["lens"], s["cu"], hq, hkv, d, 16, 0.02, 0.05)
+    clean = fq.fp8_attn_chunk(*args).view(-1, hq, d)
+    assert torch.isfinite(clean.float()).all()
+    n, lq = lens[0], q_lens[0]
+    for pos in range(n - 72, -(-n // 16) * 16):
+        head, value = pos % hkv, (pos * 7) % d
+        at = int(s["tables"][0, pos // 16]) * s["cs"] + (pos % 16 * hkv + head) * d + value
+        old = int(s["vc"][at])
+        s["vc"][at] = 0x7F
+        want = torch.zeros(clean.shape, dtype=torch.bool, device=DEV)
+        sees = torch.arange(lq, device=DEV) + n - lq >= pos
+        want[:lq, head * (hq // hkv):(head + 1) * (hq // hkv), value] = (sees & (pos < n))[:, None]
+        out = fq.fp8_attn_chunk(*args).view(-1, hq, d)
+        s["vc"][at] = old
+        assert torch.equal(torch.isnan(out.float()), want), pos
+        assert torch.equal(out[~want], clean[~want]), pos
+
+
+def test_time_does_not_go_by_codes_that_no_query_sees():
+    """Steps behind a block that does not exist: NaN codes behind the sequences' ends, seen by no one, change nothing
+    (a walk over all positions in search of them took 15 times as long; up to twice is taken for noise)."""
+    lens = [500 + (i * 2339) % 7600 for i in range(64)]
+    s = _setup([1] * 64, lens, 32, 8, 128, 32, nan_behind=False)
+    s["tables"] = s["tables"].clone()
+    s["tables"][:, 0] = -1
+    s["vc"] = (s["vc"] & 0x77).contiguous()
+    out, took = [], []
+    for stale in (False, True):
+        for b, n in enumerate(lens):
+            if stale and n % 32:
+                at = int(s["tables"][b, n // 32]) * s["cs"]
+                s["vc"][at + n % 32 * 8 * 128:at + s["cs"]] = 0x7F
+        best = math.inf
+        for _ in range(8):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            for _ in range(10):
+                o = fq.fp8_attn_chunk(s["q"], s["kc"], s["vc"], s["tables"], s["lens"], s["cu"], 32, 8, 128, 32, 0.02, 0.05)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        out.append(o)
+        took.append(best)
+    assert torch.equal(*out)
+    assert took[1] < 2 * took[0], took
