@@ -919,6 +919,8 @@ def fp8_attn_chunk(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     width = block_tables.shape[1]
     if width > 0x7FFFFFFF:
         raise ValueError(f"block_tables of {width} columns are too wide")
+    if n > 0x7FFFFFFF or block_size > 0x7FFFFFFF:
+        raise ValueError(f"{n} sequences or a block_size of {block_size} are too many")
     table_stride, inner = block_tables.stride()
     if inner != 1 and width > 1:
         raise ValueError("block_tables' rows must be packed")
