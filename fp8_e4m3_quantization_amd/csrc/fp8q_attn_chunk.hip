@@ -325,7 +325,8 @@ struct Work {
   // -infinity; s holds positions p0 .. p0 + 32 kBlocks - 1.  Returns a bit for each of the lane's positions that some
   // row of the wave sees: NaN codes of the others' values (stale ones behind a sequence's end, those of a block in
   // the place of one that does not exist) do not count, nor do they start take_nans, which goes over positions one
-  // by one (64 steps of 500 to 8100 positions behind a block that does not exist, stale codes NaN: 2850 us with it, 184 without).
+  // by one (64 steps of 500 to 8100 positions behind a block that does not exist, stale codes NaN: 2850 us with it, 186
+  // without).
   template <int kBlocks>
   __device__ __forceinline__ uint32_t mask(v16f* s, int p0, int limit) const {
     const int half = (threadIdx.x & 63) >> 5, left = limit - p0 - 4 * half;

@@ -18,9 +18,10 @@
 // steps are exact scalings of one another across binades, so it is a statement about the
 // 2^7 bf16 mantissas times the 2^23 binary32 mantissas of s, which the test suite
 // checks exhaustively on the CPU.  It holds for every binary32 x as well (rows that were not
-// rounded to bf16): the last step rounds x / s off by at most 2^-22 steps of its last place, and
-// the pairs whose quotient lies so close to a border between two numbers are all checked.  Writing the remainder with its sign flipped keeps a
-// negative zero input negative (a -0 sum would otherwise round to +0).
+// rounded to bf16): the last step rounds x / s off by little more than 2^-22 steps of its last
+// place, and the pairs whose quotient lies so close to a border between two numbers are all
+// checked.  Writing the remainder with its sign flipped keeps a negative zero input negative (a
+// -0 sum would otherwise round to +0).
 #pragma once
 #include <stdint.h>
 
